@@ -33,7 +33,9 @@ EXPORTS = ("fpx_num_blocks", "fpx_scores_elems", "fpx_rows", "fpx_max_nnz", "fpx
            "fpx_select_noalloc_max_bytes", "fpx_diag_bounded_wait", "fpx_block_scores_paged",
            "fpx_sparse_prefill_paged", "fpx_block_scores_rescue", "fpx_select_rescue",
            "fpx_diag_exp2", "fpx_pattern_words", "fpx_vs_workspace_bytes", "fpx_probe_patterns",
-           "fpx_vs_select", "fpx_vs_prefill")
+           "fpx_vs_select", "fpx_vs_prefill", "fpx_spans", "fpx_span_select", "fpx_span_prefill",
+           "fpx_page_workspace_bytes", "fpx_page_resize", "fpx_kv_append",
+           "fpx_decode_workspace_bytes", "fpx_decode")
 
 
 class FpxError(RuntimeError):
@@ -56,6 +58,25 @@ class PagedKV(ctypes.Structure):
     """Mirror of ``fpx_paged_kv``."""
     _fields_ = [("block_table_d", ctypes.c_void_p), ("pages_per_seq", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32)]
+
+
+class ScoreRule(ctypes.Structure):
+    """Mirror of ``fpx_score_rule``."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes_d", ctypes.c_void_p), ("key_lo_d", ctypes.c_void_p),
+                ("key_hi_d", ctypes.c_void_p)]
+
+
+class DecodeProblem(ctypes.Structure):
+    """Mirror of ``fpx_decode_problem``."""
+    _fields_ = [("num_seqs", ctypes.c_int32), ("q_len", ctypes.c_int32), ("hq", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+                ("k_scale_d", ctypes.c_void_p), ("v_scale_d", ctypes.c_void_p),
+                ("ctx_lens_d", ctypes.c_void_p), ("block_table_d", ctypes.c_void_p),
+                ("pages_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("group_ptr_d", ctypes.c_void_p),
+                ("prefix_pages_d", ctypes.c_void_p)]
 
 
 def paged_kv(block_table: torch.Tensor, num_pages: int) -> PagedKV:
@@ -129,6 +150,26 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fpx_select_rescue.argtypes = [P, vp, vp, vp, f32, f32, i32, i32, vp, vp, i64, vp, vp, sz,
                                       vp]
     lib.fpx_select_rescue.restype = ctypes.c_int
+    RU = ctypes.POINTER(ScoreRule)
+    D = ctypes.POINTER(DecodeProblem)
+    lib.fpx_spans.argtypes = [P, i32, vp, vp, vp, vp, vp]
+    lib.fpx_spans.restype = ctypes.c_int
+    lib.fpx_span_select.argtypes = [P, RU, vp, vp, i64, vp, vp, sz, vp]
+    lib.fpx_span_select.restype = ctypes.c_int
+    lib.fpx_span_prefill.argtypes = [P, vp, vp, vp, K, RU, vp, vp, vp, vp, vp, sz, vp]
+    lib.fpx_span_prefill.restype = ctypes.c_int
+    lib.fpx_page_workspace_bytes.argtypes = [i32]
+    lib.fpx_page_workspace_bytes.restype = sz
+    lib.fpx_page_resize.argtypes = [i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                    i32, vp, sz, vp]
+    lib.fpx_page_resize.restype = ctypes.c_int
+    lib.fpx_kv_append.argtypes = [ctypes.c_int, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i32,
+                                  vp, vp, vp, sz, vp]
+    lib.fpx_kv_append.restype = ctypes.c_int
+    lib.fpx_decode_workspace_bytes.argtypes = [D]
+    lib.fpx_decode_workspace_bytes.restype = sz
+    lib.fpx_decode.argtypes = [D, vp, vp, vp, RU, vp, vp, vp, sz, vp]
+    lib.fpx_decode.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -449,3 +490,333 @@ def vs_path(q, k, v, block: int, n_probe: int, alpha_v: float, alpha_s: float, c
     check(status(ws, stream), "device status")
     return dict(problem=pf, vert=vert, slash=slash, row_ptr=row_ptr, col_idx=col_idx, nnz=nnz,
                 o=o, lse=lse)
+
+
+# ---- attention under a score rule -----------------------------------------------------------
+
+def _expect(name: str, t: Optional[torch.Tensor], dtype, device=None, numel: int = 0,
+            shape=None) -> None:
+    """Refuses a tensor that the device code would misread (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} entries, needs {numel}")
+
+
+class _On:
+    """Launches go to `device`: makes it current if it is not; the stream defaults to its own."""
+
+    def __init__(self, device, stream):
+        self.index = device.index if device.index is not None else torch.cuda.current_device()
+        self.stream = stream
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.index)
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+        return False
+
+
+def score_rule(softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
+               key_lo: Optional[torch.Tensor] = None,
+               key_hi: Optional[torch.Tensor] = None) -> ScoreRule:
+    """What a layer does to its scores: a tanh cap, a bias -slopes[h] * |i - j| (fp32 [Hq]), the
+    last `window` positions only, and key spans (int32 [query tokens] each, as ``spans`` writes
+    them; None: keys 0 .. i).  The tensors must live as long as the rule is used."""
+    _expect("slopes", slopes, torch.float32)
+    _expect("key_lo", key_lo, torch.int32)
+    _expect("key_hi", key_hi, torch.int32)
+    if (key_lo is None) != (key_hi is None):
+        raise ValueError("key_lo and key_hi come together")
+    r = ScoreRule(float(softcap), int(window), _ptr(slopes), _ptr(key_lo), _ptr(key_hi))
+    r._keep = (slopes, key_lo, key_hi)
+    return r
+
+
+def _check_rule(rule: ScoreRule, hq: int, tokens: int, device) -> None:
+    slopes, lo, hi = getattr(rule, "_keep", (None, None, None))
+    _expect("slopes", slopes, torch.float32, device, hq)
+    _expect("key_lo", lo, torch.int32, device, tokens)
+    _expect("key_hi", hi, torch.int32, device, tokens)
+
+
+def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
+          prefix: Optional[torch.Tensor] = None, key_lo: Optional[torch.Tensor] = None,
+          key_hi: Optional[torch.Tensor] = None, device=None, stream=None):
+    """fpx_spans -> (key_lo, key_hi) int32 [T]: each document (doc_cu int32 [documents + 1] token
+    offsets; None: each sequence) attends itself, causally but for its first prefix[document]
+    tokens.  `device` is needed only where no tensor names one."""
+    given = [t for t in (key_lo, key_hi, doc_cu, prefix, pf.cu_d) if t is not None]
+    dev = given[0].device if given else torch.device(device or "cuda")
+    total = pf.struct.total_tokens
+    docs = 0 if doc_cu is None else doc_cu.numel() - 1
+    if doc_cu is not None and docs < 1:
+        raise ValueError("doc_cu needs at least one document")
+    _expect("doc_cu", doc_cu, torch.int32, dev)
+    _expect("prefix", prefix, torch.int32, dev, docs if doc_cu is not None else pf.struct.num_seqs)
+    key_lo = torch.empty(total, dtype=torch.int32, device=dev) if key_lo is None else key_lo
+    key_hi = torch.empty(total, dtype=torch.int32, device=dev) if key_hi is None else key_hi
+    _expect("key_lo", key_lo, torch.int32, dev, total)
+    _expect("key_hi", key_hi, torch.int32, dev, total)
+    with _On(dev, stream) as s:
+        check(load().fpx_spans(pf.ptr, docs, _ptr(doc_cu), _ptr(prefix), _ptr(key_lo),
+                               _ptr(key_hi), s), "fpx_spans")
+    return key_lo, key_hi
+
+
+def span_capacity(pf: Prefill) -> int:
+    """CSR entries that a rule can need at most: Hq * sum of (blocks of a sequence)^2."""
+    b = pf.struct.block
+    lens = np.diff(pf.cu_h.astype(np.int64)) if pf.cu_h is not None else \
+        np.array([pf.struct.total_tokens], dtype=np.int64)
+    return int(pf.struct.hq * ((-(-lens // b)) ** 2).sum())
+
+
+def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, col_idx=None,
+                nnz=None, capacity: Optional[int] = None, stream=None):
+    """fpx_span_select -> (row_ptr, col_idx, nnz): the key blocks that the rule's spans reach."""
+    dev = ws.device
+    _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, dev)
+    if row_ptr is None:
+        row_ptr = torch.empty(pf.rows + 1, dtype=torch.int32, device=dev)
+    if col_idx is None:
+        cap = span_capacity(pf) if capacity is None else capacity
+        col_idx = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
+    cap = col_idx.numel() if capacity is None else capacity
+    if nnz is None:
+        nnz = torch.empty(1, dtype=torch.int64, device=dev)
+    _check_csr_outputs(pf, row_ptr, col_idx, nnz, cap)
+    with _On(dev, stream) as s:
+        check(load().fpx_span_select(pf.ptr, ctypes.byref(rule), _ptr(row_ptr), _ptr(col_idx), cap,
+                                     _ptr(nnz), _ptr(ws), ws.numel(), s), "fpx_span_select")
+    return row_ptr, col_idx, nnz
+
+
+def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rule: ScoreRule,
+                 row_ptr: torch.Tensor, col_idx: torch.Tensor, ws: torch.Tensor,
+                 kv: Optional[PagedKV] = None, o: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """fpx_span_prefill -> (O, LSE): attention over the listed blocks under the rule.  K and V are
+    packed, or with `kv` the page caches."""
+    p, dev = pf.struct, q.device
+    _expect("q", q, q.dtype, dev, shape=(p.total_tokens, p.hq, p.d))
+    rows = kv.num_pages * p.block if kv is not None else p.total_tokens
+    for name, t in (("k", k), ("v", v)):
+        _expect(name, t, q.dtype, dev)
+        if t.numel() != rows * p.hkv * p.d:
+            raise ValueError(f"{name} must hold {rows} rows of [{p.hkv}, {p.d}]")
+    if _DTYPES[q.dtype] != p.dtype:
+        raise TypeError(f"q is {q.dtype}, the problem was described with another type")
+    _check_rule(rule, p.hq, p.total_tokens, dev)
+    _expect("row_ptr", row_ptr, torch.int32, dev, pf.rows + 1)
+    _expect("col_idx", col_idx, torch.int32, dev)
+    odt = torch.float32 if q.dtype == torch.float32 else torch.bfloat16
+    o = torch.empty(q.shape, dtype=odt, device=dev) if o is None else o
+    if lse is None and want_lse:
+        lse = torch.empty((p.hq, p.total_tokens), dtype=torch.float32, device=dev)
+    _expect("o", o, odt, dev, shape=q.shape)
+    _expect("lse", lse, torch.float32, dev, p.hq * p.total_tokens)
+    with _On(dev, stream) as s:
+        check(load().fpx_span_prefill(pf.ptr, _ptr(q), _ptr(k), _ptr(v),
+                                      ctypes.byref(kv) if kv is not None else None,
+                                      ctypes.byref(rule), _ptr(row_ptr), _ptr(col_idx), _ptr(o),
+                                      _ptr(lse), _ptr(ws), ws.numel(), s), "fpx_span_prefill")
+    return o, lse
+
+
+def span_path(q, k, v, block: int, cu_seqlens=None, doc_cu=None, prefix=None, softcap: float = 0.0,
+              slopes=None, window: int = 0, softmax_scale: float = 0.0, q_scale=None, k_scale=None,
+              v_scale=None, stream=None) -> dict:
+    """The whole path under a rule on one stream: spans -> blocks -> O, LSE.  Raises on any
+    recorded error."""
+    with _On(q.device, stream):
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device)
+        pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
+        ws = workspace(pf, -1, q.device)
+        lo, hi = spans(pf, doc_cu, prefix, device=q.device, stream=stream)
+        rule = score_rule(softcap, slopes, window, lo, hi)
+        row_ptr, col_idx, nnz = span_select(pf, rule, ws, stream=stream)
+        o, lse = span_prefill(pf, q, k, v, rule, row_ptr, col_idx, ws, stream=stream)
+        check(status(ws, stream), "device status")
+    return dict(problem=pf, rule=rule, row_ptr=row_ptr, col_idx=col_idx, nnz=nnz, o=o, lse=lse)
+
+
+# ---- paged cache and decode -----------------------------------------------------------------
+
+def page_workspace(num_seqs: int, device=None) -> torch.Tensor:
+    """A zeroed workspace for fpx_page_resize (up to num_seqs requests) and fpx_kv_append."""
+    n = load().fpx_page_workspace_bytes(int(num_seqs))
+    if n == 0:
+        raise FpxError(-1, "fpx_page_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                free_pages: torch.Tensor, free_count: torch.Tensor, page: int, num_pages: int,
+                token_capacity: int, ws: torch.Tensor, keep_pages=None, count_out=None,
+                cu_new=None, slots=None, positions=None, stream=None):
+    """fpx_page_resize: requests grow or shrink from lens to new_lens -> (cu_new int32 [S + 1],
+    slots int32 [token_capacity], positions int32 [token_capacity]).  block_table, free_pages and
+    the count (count_out, by default free_count itself) are updated."""
+    dev, n = lens.device, lens.numel()
+    count_out = free_count if count_out is None else count_out
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be [num_seqs, pages_per_seq]")
+    for name, t, need in (("lens", lens, n), ("new_lens", new_lens, n),
+                          ("keep_pages", keep_pages, n), ("block_table", block_table, 0),
+                          ("free_pages", free_pages, num_pages), ("free_count", free_count, 1),
+                          ("count_out", count_out, 1)):
+        _expect(name, t, torch.int32, dev, need)
+    cu_new = torch.empty(n + 1, dtype=torch.int32, device=dev) if cu_new is None else cu_new
+    if slots is None:
+        slots = torch.empty(token_capacity, dtype=torch.int32, device=dev)
+    if positions is None:
+        positions = torch.empty(token_capacity, dtype=torch.int32, device=dev)
+    for name, t, need in (("cu_new", cu_new, n + 1), ("slots", slots, token_capacity),
+                          ("positions", positions, token_capacity)):
+        _expect(name, t, torch.int32, dev, need)
+    with _On(dev, stream) as s:
+        check(load().fpx_page_resize(n, int(page), int(num_pages), _ptr(lens), _ptr(new_lens),
+                                     _ptr(keep_pages), _ptr(block_table), block_table.shape[1],
+                                     _ptr(free_pages), _ptr(free_count), _ptr(count_out),
+                                     _ptr(cu_new), _ptr(slots), _ptr(positions),
+                                     int(token_capacity), _ptr(ws), ws.numel(), s),
+              "fpx_page_resize")
+    return cu_new, slots, positions
+
+
+def _cache_rows(name: str, t: torch.Tensor, hkv: int, d: int, device) -> int:
+    if t.dim() < 3 or t.shape[-1] != d or t.shape[-2] != hkv:
+        raise ValueError(f"{name} must be [.., {hkv}, {d}], got {tuple(t.shape)}")
+    _expect(name, t, t.dtype, device)
+    return t.numel() // (hkv * d)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, ws: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """fpx_kv_append: rows k, v [n, Hkv, D] (each row contiguous; the rows may be strided, as slices
+    of a projection's output are) into cache rows slots[n].  e4m3 caches take bf16 rows and the
+    heads' scales (fp32 [Hkv])."""
+    dev, (n, hkv, d) = k.device, k.shape
+    if k_cache.dtype not in _DTYPES:
+        raise TypeError(f"unsupported cache type {k_cache.dtype}")
+    src = torch.float32 if k_cache.dtype == torch.float32 else torch.bfloat16
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != src or t.device != dev or tuple(t.shape) != (n, hkv, d):
+            raise ValueError(f"{name} must be {src} {(n, hkv, d)} on {dev}")
+        if n > 0 and (t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d)):
+            raise ValueError(f"a row of {name} must be contiguous")
+    rows = _cache_rows("k_cache", k_cache, hkv, d, dev)
+    if _cache_rows("v_cache", v_cache, hkv, d, dev) != rows or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have the same rows and type")
+    _expect("slots", slots, torch.int32, dev, n)
+    _expect("k_scale", k_scale, torch.float32, dev, hkv)
+    _expect("v_scale", v_scale, torch.float32, dev, hkv)
+    ks, vs = (t.stride(0) if n > 1 else hkv * d for t in (k, v))
+    with _On(dev, stream) as s:
+        check(load().fpx_kv_append(_DTYPES[k_cache.dtype], hkv, d, n, _ptr(k), ks, _ptr(v), vs,
+                                   _ptr(slots), _ptr(k_cache), _ptr(v_cache), rows, _ptr(k_scale),
+                                   _ptr(v_scale), _ptr(ws), ws.numel(), s), "fpx_kv_append")
+
+
+@dataclass
+class Decode:
+    """One decode problem bound to device tensors (keeps them and the struct alive)."""
+    struct: DecodeProblem
+    keep: tuple
+    q_shape: tuple
+    q_dtype: torch.dtype
+    device: torch.device
+
+    @property
+    def ptr(self):
+        return ctypes.byref(self.struct)
+
+
+def decode_problem(q: torch.Tensor, k_cache: torch.Tensor, ctx_lens: torch.Tensor,
+                   block_table: torch.Tensor, q_len: int = 1, softmax_scale: float = 0.0,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                   group_ptr: Optional[torch.Tensor] = None,
+                   prefix_pages: Optional[torch.Tensor] = None) -> Decode:
+    """Describes Q [S * q_len, Hq, D] against caches [num_pages, page, Hkv, D] (page tables int32
+    [S, pages_per_seq], lengths int32 [S]); group_ptr int32 [G + 1] and prefix_pages int32 [G] name
+    runs of requests that share their first pages."""
+    if k_cache.dtype not in _DTYPES:
+        raise TypeError(f"unsupported cache type {k_cache.dtype}")
+    if k_cache.dim() != 4 or q.dim() != 3:
+        raise ValueError("k_cache must be [num_pages, page, Hkv, D] and q [tokens, Hq, D]")
+    dev, n = q.device, ctx_lens.numel()
+    num_pages, page, hkv, d = k_cache.shape
+    if q.shape[0] != n * q_len or q.shape[2] != d:
+        raise ValueError(f"q must be [{n} * {q_len}, Hq, {d}], got {tuple(q.shape)}")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be [num_seqs, pages_per_seq]")
+    if (group_ptr is None) != (prefix_pages is None):
+        raise ValueError("group_ptr and prefix_pages come together")
+    groups = 0 if group_ptr is None else group_ptr.numel() - 1
+    if group_ptr is not None and groups < 1:
+        raise ValueError("group_ptr needs at least one group")
+    for name, t, dt, need in (("ctx_lens", ctx_lens, torch.int32, n),
+                              ("block_table", block_table, torch.int32, 0),
+                              ("k_scale", k_scale, torch.float32, hkv),
+                              ("v_scale", v_scale, torch.float32, hkv),
+                              ("group_ptr", group_ptr, torch.int32, 0),
+                              ("prefix_pages", prefix_pages, torch.int32, groups)):
+        _expect(name, t, dt, dev, need)
+    s = DecodeProblem(n, int(q_len), q.shape[1], hkv, d, page, _DTYPES[k_cache.dtype],
+                      float(softmax_scale), _ptr(k_scale), _ptr(v_scale), _ptr(ctx_lens),
+                      _ptr(block_table), block_table.shape[1], num_pages, groups, _ptr(group_ptr),
+                      _ptr(prefix_pages))
+    qdt = torch.float32 if k_cache.dtype == torch.float32 else torch.bfloat16
+    return Decode(s, (ctx_lens, block_table, k_scale, v_scale, group_ptr, prefix_pages),
+                  tuple(q.shape), qdt, dev)
+
+
+def decode_workspace(dp: Decode) -> torch.Tensor:
+    """A zeroed workspace for fpx_decode."""
+    n = load().fpx_decode_workspace_bytes(dp.ptr)
+    if n == 0:
+        raise FpxError(-2, "fpx_decode_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=dp.device)
+
+
+def decode(dp: Decode, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+           ws: torch.Tensor, rule: Optional[ScoreRule] = None, o: Optional[torch.Tensor] = None,
+           lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """fpx_decode -> (O [S * q_len, Hq, D], LSE fp32 [Hq, S * q_len])."""
+    p, dev = dp.struct, dp.device
+    tokens = dp.q_shape[0]
+    _expect("q", q, dp.q_dtype, dev, shape=dp.q_shape)
+    shape = (p.num_pages, p.page, p.hkv, p.d)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if _DTYPES.get(t.dtype) != p.dtype:
+            raise TypeError(f"{name} is {t.dtype}, the problem was described with another type")
+        _expect(name, t, t.dtype, dev, shape=shape)
+    if rule is not None:
+        _check_rule(rule, p.hq, tokens, dev)
+    o = torch.empty(dp.q_shape, dtype=dp.q_dtype, device=dev) if o is None else o
+    if lse is None and want_lse:
+        lse = torch.empty((p.hq, tokens), dtype=torch.float32, device=dev)
+    _expect("o", o, dp.q_dtype, dev, shape=dp.q_shape)
+    _expect("lse", lse, torch.float32, dev, p.hq * tokens)
+    with _On(dev, stream) as s:
+        check(load().fpx_decode(dp.ptr, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                ctypes.byref(rule) if rule is not None else None, _ptr(o),
+                                _ptr(lse), _ptr(ws), ws.numel(), s), "fpx_decode")
+    return o, lse

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "fpx_decode.cuh"
 #include "fpx_internal.h"
 
 using namespace fpx;
@@ -99,6 +100,68 @@ fpx_status apply_paged(const fpx_problem* p, const Sizes& s, const fpx_paged_kv*
   return FPX_OK;
 }
 
+// Host checks of a score rule; fills the kernels' form.
+fpx_status check_rule(const fpx_score_rule* r, RuleDesc* d) {
+  if (!std::isfinite(r->softcap) || r->softcap < 0.f || r->window < 0) return FPX_ERR_INVALID_ARG;
+  if ((r->key_lo_d == nullptr) != (r->key_hi_d == nullptr)) return FPX_ERR_INVALID_ARG;
+  if (!aligned(r->slopes_d, 4) || !aligned(r->key_lo_d, 4) || !aligned(r->key_hi_d, 4))
+    return FPX_ERR_ALIGNMENT;
+  d->softcap = r->softcap;
+  d->window = r->window;
+  d->slopes = r->slopes_d;
+  d->lo = r->key_lo_d;
+  d->hi = r->key_hi_d;
+  return FPX_OK;
+}
+
+// Host checks of a decode problem; fills the kernels' form.
+fpx_status check_decode(const fpx_decode_problem* p, decode::DecodeDesc* d) {
+  if (!p) return FPX_ERR_INVALID_ARG;
+  if (p->dtype != FPX_F32 && p->dtype != FPX_BF16 && p->dtype != FPX_E4M3)
+    return FPX_ERR_UNSUPPORTED;
+  if (p->d != 64 && p->d != 128) return FPX_ERR_UNSUPPORTED;
+  if (!is_pow2(p->page) || p->page < 16 || p->page > 128) return FPX_ERR_UNSUPPORTED;
+  if (p->num_seqs < 1 || p->q_len < 1 || p->hq < 1 || p->hkv < 1 || p->hq % p->hkv != 0 ||
+      p->pages_per_seq < 1 || p->num_pages < 1 || p->num_groups < 0)
+    return FPX_ERR_INVALID_ARG;
+  if (!p->ctx_lens_d || !p->block_table_d) return FPX_ERR_INVALID_ARG;
+  if (p->num_groups > 0 && (!p->group_ptr_d || !p->prefix_pages_d)) return FPX_ERR_INVALID_ARG;
+  const bool quant = p->dtype == FPX_E4M3;
+  if (quant != (p->k_scale_d != nullptr) || quant != (p->v_scale_d != nullptr))
+    return FPX_ERR_INVALID_ARG;
+  if (!std::isfinite(p->softmax_scale)) return FPX_ERR_INVALID_ARG;
+  if (!aligned(p->ctx_lens_d, 4) || !aligned(p->block_table_d, 4) || !aligned(p->group_ptr_d, 4) ||
+      !aligned(p->prefix_pages_d, 4) || !aligned(p->k_scale_d, 4) || !aligned(p->v_scale_d, 4))
+    return FPX_ERR_ALIGNMENT;
+  // int32 cache rows, key positions, rows of the output and grid sizes
+  if (static_cast<int64_t>(p->num_pages) * p->page > INT32_MAX ||
+      static_cast<int64_t>(p->pages_per_seq) * p->page > INT32_MAX / 2 ||
+      static_cast<int64_t>(p->num_seqs) * p->q_len > INT32_MAX / p->hq || p->num_groups > p->num_seqs)
+    return FPX_ERR_UNSUPPORTED;
+  d->num_seqs = p->num_seqs;
+  d->q_len = p->q_len;
+  d->hq = p->hq;
+  d->hkv = p->hkv;
+  d->group = p->hq / p->hkv;
+  d->d = p->d;
+  d->page = p->page;
+  d->log2_page = 0;
+  while ((1 << d->log2_page) < p->page) ++d->log2_page;
+  d->pages_per_seq = p->pages_per_seq;
+  d->num_pages = p->num_pages;
+  d->num_groups = p->num_groups;
+  d->tokens = p->num_seqs * p->q_len;
+  d->scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->d));
+  d->k_scale = p->k_scale_d;
+  d->v_scale = p->v_scale_d;
+  d->ctx = p->ctx_lens_d;
+  d->table = p->block_table_d;
+  d->group_ptr = p->group_ptr_d;
+  d->prefix_pages = p->prefix_pages_d;
+  d->rule = RuleDesc{};
+  return decode_fits(*d, p->dtype) ? FPX_OK : FPX_ERR_UNSUPPORTED;
+}
+
 // Keep bitmask of the select stage: one 32-bit word per 32 key blocks of the longest row.
 int64_t mask_words(const Sizes& s) { return (s.nb_max + 31) / 32; }
 
@@ -117,6 +180,27 @@ size_t scratch_bytes(const fpx_problem* p, const Sizes& s, int which) {
     default:
       return 0;
   }
+}
+
+// The select stage's scratch inside a workspace, laid out as scratch_bytes(.., 1) counts it.
+struct SelectScratch {
+  int32_t* counts;
+  int64_t* cta_tot;
+  int* overflow;
+  uint32_t* mask;
+};
+
+SelectScratch select_scratch(const fpx_problem* p, const Sizes& s, void* ws) {
+  const size_t R = static_cast<size_t>(s.nb) * p->hq;
+  char* at = static_cast<char*>(ws) + scratch_offset(p->num_seqs) + align_up(sizeof(float) * R, 256);
+  SelectScratch x;
+  x.counts = reinterpret_cast<int32_t*>(at);
+  at += align_up(sizeof(int32_t) * R, 256);
+  x.cta_tot = reinterpret_cast<int64_t*>(at);
+  at += align_up(sizeof(int64_t) * (R / 8 + 1), 256);
+  x.overflow = reinterpret_cast<int*>(at);
+  x.mask = reinterpret_cast<uint32_t*>(at + 256);
+  return x;
 }
 
 size_t ws_bytes_for(const fpx_problem* p, const Sizes& s, int which) {
@@ -371,7 +455,8 @@ static fpx_status sparse_prefill_impl(const fpx_problem* p, const void* q, const
                                       const int32_t* row_ptr, const int32_t* col_idx, void* o,
                                       float* lse, void* ws, size_t ws_bytes,
                                       fpx_stream_t stream, const uint32_t* vbits = nullptr,
-                                      const uint32_t* sbits = nullptr) {
+                                      const uint32_t* sbits = nullptr,
+                                      const fpx_score_rule* rule = nullptr) {
   Sizes sz;
   fpx_status rc = check_problem(p, &sz);
   if (rc != FPX_OK) return rc;
@@ -382,6 +467,11 @@ static fpx_status sparse_prefill_impl(const fpx_problem* p, const void* q, const
     return FPX_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   ProblemDesc d = make_desc(p, sz);
+  RuleDesc rd;
+  if (rule) {
+    if ((rc = check_rule(rule, &rd)) != FPX_OK) return rc;
+    if (p->total_tokens > 0 && !col_idx) return FPX_ERR_INVALID_ARG;
+  }
   if (kv) {
     if ((rc = apply_paged(p, sz, kv, &d)) != FPX_OK) return rc;
     if (!attn_tc_supported(d, p->dtype)) return FPX_ERR_UNSUPPORTED;  // paged: tensor-core path
@@ -401,12 +491,13 @@ static fpx_status sparse_prefill_impl(const fpx_problem* p, const void* q, const
   if (tc) {
     bool encode_failed = false;
     cudaError_t e = launch_attn_tc(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order,
-                                   queue_head, vbits, sbits, pattern_words(p), st, s,
+                                   queue_head, vbits, sbits, pattern_words(p), rule ? &rd : nullptr, st, s,
                                    &encode_failed);
     if (encode_failed) return FPX_ERR_UNSUPPORTED;
     return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
   }
-  return launch_attn_simt(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order, st, s) == cudaSuccess
+  return launch_attn_simt(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order,
+                          rule ? &rd : nullptr, st, s) == cudaSuccess
              ? FPX_OK
              : FPX_ERR_CUDA;
 }
@@ -519,6 +610,85 @@ fpx_status fpx_vs_prefill(const fpx_problem* p, const void* q, const void* k, co
   if (!aligned(vert_bits, 4) || !aligned(slash_bits, 4)) return FPX_ERR_ALIGNMENT;
   return sparse_prefill_impl(p, q, k, v, nullptr, row_ptr, col_idx, o, lse, ws, ws_bytes, stream,
                              vert_bits, slash_bits);
+}
+
+fpx_status fpx_spans(const fpx_problem* p, int32_t num_docs, const int32_t* doc_cu_d,
+                     const int32_t* prefix_d, int32_t* key_lo, int32_t* key_hi,
+                     fpx_stream_t stream) {
+  Sizes sz;
+  fpx_status rc = check_problem(p, &sz);
+  if (rc != FPX_OK) return rc;
+  if (num_docs < 0 || (num_docs == 0) != (doc_cu_d == nullptr)) return FPX_ERR_INVALID_ARG;
+  if (p->total_tokens > 0 && (!key_lo || !key_hi)) return FPX_ERR_INVALID_ARG;
+  if (!aligned(doc_cu_d, 4) || !aligned(prefix_d, 4) || !aligned(key_lo, 4) || !aligned(key_hi, 4))
+    return FPX_ERR_ALIGNMENT;
+  return launch_spans(make_desc(p, sz), num_docs, doc_cu_d, prefix_d, key_lo, key_hi,
+                      reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FPX_OK
+             : FPX_ERR_CUDA;
+}
+
+fpx_status fpx_span_select(const fpx_problem* p, const fpx_score_rule* rule, int32_t* row_ptr,
+                           int32_t* col_idx, int64_t col_capacity, int64_t* nnz_d, void* ws,
+                           size_t ws_bytes, fpx_stream_t stream) {
+  Sizes sz;
+  fpx_status rc = check_problem(p, &sz);
+  if (rc != FPX_OK) return rc;
+  if (!rule) return FPX_ERR_INVALID_ARG;
+  RuleDesc rd;
+  if ((rc = check_rule(rule, &rd)) != FPX_OK) return rc;
+  if ((rc = check_ws(p, sz, 1, ws, ws_bytes)) != FPX_OK) return rc;
+  if (col_capacity < 0 || col_capacity > INT32_MAX || !row_ptr) return FPX_ERR_INVALID_ARG;
+  if (p->total_tokens > 0 && !col_idx && col_capacity > 0) return FPX_ERR_INVALID_ARG;
+  if (!aligned(row_ptr, 4) || !aligned(col_idx, 4) || !aligned(nnz_d, 8))
+    return FPX_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const ProblemDesc d = make_desc(p, sz);
+  StatusBlock* st = static_cast<StatusBlock*>(ws);
+  const SeqTables t = seq_tables_at(ws, p->num_seqs);
+  const SelectScratch x = select_scratch(p, sz, ws);
+  if (launch_plan(d, t, st, s) != cudaSuccess) return FPX_ERR_CUDA;
+  const int mw = static_cast<int>(mask_words(sz));
+  if (launch_span_count(d, rd, t, x.counts, x.cta_tot, x.mask, mw, s) != cudaSuccess)
+    return FPX_ERR_CUDA;
+  return launch_select_finish(d, row_ptr, col_idx, col_capacity, nnz_d, x.counts, x.cta_tot,
+                              x.overflow, x.mask, mw, t, st, s, true) == cudaSuccess
+             ? FPX_OK
+             : FPX_ERR_CUDA;
+}
+
+fpx_status fpx_span_prefill(const fpx_problem* p, const void* q, const void* k, const void* v,
+                            const fpx_paged_kv* kv, const fpx_score_rule* rule,
+                            const int32_t* row_ptr, const int32_t* col_idx, void* o, float* lse,
+                            void* ws, size_t ws_bytes, fpx_stream_t stream) {
+  if (!rule) return FPX_ERR_INVALID_ARG;
+  return sparse_prefill_impl(p, q, k, v, kv, row_ptr, col_idx, o, lse, ws, ws_bytes, stream,
+                             nullptr, nullptr, rule);
+}
+
+size_t fpx_decode_workspace_bytes(const fpx_decode_problem* p) {
+  decode::DecodeDesc d;
+  return check_decode(p, &d) == FPX_OK ? decode_workspace(d, p->dtype) : 0;
+}
+
+fpx_status fpx_decode(const fpx_decode_problem* p, const void* q, const void* k_cache,
+                      const void* v_cache, const fpx_score_rule* rule, void* o, float* lse,
+                      void* ws, size_t ws_bytes, fpx_stream_t stream) {
+  decode::DecodeDesc d;
+  fpx_status rc = check_decode(p, &d);
+  if (rc != FPX_OK) return rc;
+  if (rule && (rc = check_rule(rule, &d.rule)) != FPX_OK) return rc;
+  if (!q || !k_cache || !v_cache || !o || !ws) return FPX_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(ws, 256))
+    return FPX_ERR_ALIGNMENT;
+  if (ws_bytes < decode_workspace(d, p->dtype)) return FPX_ERR_CAPACITY;
+  bool encode_failed = false;
+  const cudaError_t e =
+      launch_decode(d, p->dtype, q, k_cache, v_cache, o, lse, ws, static_cast<StatusBlock*>(ws),
+                    reinterpret_cast<cudaStream_t>(stream), &encode_failed);
+  if (encode_failed) return FPX_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
 }
 
 fpx_status fpx_sparse_prefill_paged(const fpx_problem* p, const void* q, const void* k_cache,

@@ -231,6 +231,12 @@ __device__ __forceinline__ Unit decode_unit(const ProblemDesc& p, const int32_t*
   return w;
 }
 
+// Last key block that a CSR row of the unit may list.
+template <bool kRule>
+__device__ __forceinline__ int last_block(const Unit& w) {
+  return kRule ? (w.n_s - 1) / kTileN : w.I;
+}
+
 // 128 bits [bit0, bit0 + 128) of a bitmask row of `words` words, as four words (bit c of the
 // result in word c / 32); bits outside the row read as 0.
 __device__ __forceinline__ void bits128(const uint32_t* __restrict__ row, int words, int64_t bit0,
@@ -250,7 +256,10 @@ __device__ __forceinline__ void bits128(const uint32_t* __restrict__ row, int wo
 // kMask: the vertical / slash token mask (query i of sequence s attends key j <= i iff bit
 // s_start + j of vbits[h] or bit s_start + (i - j) of sbits[h] is set) is applied inside every
 // listed key block, and a row that no key reaches gets O = 0, LSE = -inf.
-template <bool kFp8, bool kMask>
+// kRule: the score rule (cap, distance bias, key spans and window) replaces the causal mask and the
+// listed blocks may lie above the diagonal.  The rule's transform runs on the S row in registers
+// between the TMEM load and the row maximum.
+template <bool kFp8, bool kMask, bool kRule>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, ProblemDesc p,
@@ -258,10 +267,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                __nv_bfloat16* __restrict__ o, float* __restrict__ lse, SeqTables tab,
                const int32_t* __restrict__ order, int* __restrict__ queue_head, int n_units,
                const uint32_t* __restrict__ vbits, const uint32_t* __restrict__ sbits, int words,
-               StatusBlock* st) {
+               RuleDesc rule, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
   using C = Cfg<kFp8>;
   constexpr unsigned kFull = 0xffffffffu;
+  constexpr bool kMayBeEmpty = kMask || kRule;  // a row may see no key of the listed blocks
   if (!*tab.valid) return;  // inconsistent cu_seqlens (recorded by the plan kernel)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -368,7 +378,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       }
       ++q_loads;
-      RowMerge m(col_idx, w.beg[0], w.end[0], w.beg[1], w.end[1], w.I);
+      RowMerge m(col_idx, w.beg[0], w.end[0], w.beg[1], w.end[1],
+                 last_block<kRule>(w));
       int J, uses;
       while (m.next(J, uses)) {
         const int slot = n & 1;
@@ -465,7 +476,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       ++k;
       if (u < 0) break;
       const Unit w = decode_unit(p, tab.blk_base, row_ptr, u);
-      RowMerge m(col_idx, w.beg[0], w.end[0], w.beg[1], w.end[1], w.I);
+      RowMerge m(col_idx, w.beg[0], w.end[0], w.beg[1], w.end[1],
+                 last_block<kRule>(w));
       int J, uses;
       bool have = m.next(J, uses);
       if (!__all_sync(kFull, mbar_wait(bar(kBarQ), (k - 1) & 1, abort_flag))) { ok = false; break; }
@@ -613,13 +625,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         sl2 *= p.q_scale[my_h] * p.k_scale[w.kvh];
         vsc = p.v_scale[w.kvh];
       }
+      ScoreMap map = {};
+      KeySpan span = {0, -1};
+      bool mapped = false;
+      if (kRule) {
+        float scale = p.scale;
+        if (kFp8) scale *= p.q_scale[my_h] * p.k_scale[w.kvh];
+        map = score_map(rule, scale, my_h);
+        if (write) span = rule_span(rule, tq, qpos, w.n_s);
+        if (span.lo > span.hi) span = {0, -1};
+        // a rule without cap and bias leaves S as it is, and the scale stays in the exponent
+        mapped = map.cap2 != 0.f || map.slope2 != 0.f;
+        sl2 = mapped ? 1.f : map.k;
+      }
       float m_ref = -CUDART_INF_F, l_run = 0.f;
       const uint32_t* vrow = kMask ? vbits + static_cast<int64_t>(my_h) * words : nullptr;
       const uint32_t* srow = kMask ? sbits + static_cast<int64_t>(my_h) * words : nullptr;
       it = 0;
       for (int e = w.beg[t]; e < w.end[t]; ++e) {
         const int J = col_idx[e];
-        if (J < 0 || J > w.I) {
+        if (J < 0 || J > last_block<kRule>(w)) {
           if (row == 0) record_error(st, FPX_ERR_DEVICE_INPUT, 30, my_r, J);
           continue;
         }
@@ -636,9 +661,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (!mbar_wait(bar(kBarSFull + t), s_phase, abort_flag)) { ok = false; break; }
         s_phase ^= 1;
         tc_fence_after();
-        const bool diag = (J == w.I);
+        const bool diag = !kRule && (J == w.I);
+        // columns [c_lo, c_hi] of the block are seen by this row; no lane tests them where every
+        // row of the warp sees the whole block
+        const int c_lo = kRule ? span.lo - J * kTileN : 0, c_hi = kRule ? span.hi - J * kTileN : 0;
+        const bool partial = kRule && __any_sync(kFull, c_lo > 0 || c_hi < kTileN - 1);
+        const float rel = static_cast<float>(qpos - J * kTileN);
         // token causal mask (key column > query row) and token mask of one 64-column half
         auto mask_half = [&](uint32_t* x, int j0) {
+          if (kRule) {
+            if (mapped) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                x[j] = __float_as_uint(map(__uint_as_float(x[j]), fabsf(rel - (j0 + j))));
+            }
+            if (partial) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (j0 + j < c_lo || j0 + j > c_hi) x[j] = __float_as_uint(-CUDART_INF_F);
+            }
+          }
           if (diag) {
 #pragma unroll
             for (int j = 0; j < 64; ++j)
@@ -660,7 +702,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // stored yet, S is still in TMEM, and the warp redoes the block in two passes.  (bf16
         // keeps the two-pass order: its P is twice as many TMEM columns, and storing the first
         // half while the second is formed was measured to be worth more than the single pass.)
-        const bool spec = kFp8 && it > 0 && __all_sync(kFull, m_ref != -CUDART_INF_F);
+        const bool spec = kFp8 && !kRule && it > 0 && __all_sync(kFull, m_ref != -CUDART_INF_F);
         bool redo = !spec;
         if (spec) {
           tmem_ld32(tS, r);
@@ -701,8 +743,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tmem_wait_ld(r + 64);
           tmem_wait_ld(r + 96);
           mask_half(r + 64, 64);
-          // finite unless kMask: key 0 of a block row is always visible without the token
-          // mask; with it a row may see no key yet (m_ref = -inf), and -inf then stands for
+          // finite unless kMayBeEmpty: key 0 of a block row is always visible without the token
+          // mask and the rule; with them a row may see no key yet (m_ref = -inf), and -inf then stands for
           // "none"
           const float mx = fmaxf(mx_lo, row_max64(r + 64)) * sl2;
           // lazy rescale: move the reference max only when the block max exceeds it by > 2^8
@@ -728,7 +770,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           // first half of P stored while the second half is computed
           // (a row that no key has reached yet: exponents of -inf, P = 0, and the weights the
           // FMA-pipe exp2 gives them are cleared by the rescale that its first key triggers)
-          const float neg_m = (kMask && m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
+          const float neg_m = (kMayBeEmpty && m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
           rs = softmax_part_to_p<kFp8, 0, 64>(r, sl2, neg_m);
           if (kFp8) tmem_st16(tS, r);
           else tmem_st32(tS, r);
@@ -757,10 +799,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (!mbar_wait(bar(kBarODone + t), od_phase, abort_flag)) { ok = false; break; }
       od_phase ^= 1;
       tc_fence_after();
-      // kMask: a row that no key reached (blocks were listed, the token mask removed every key
+      // kMayBeEmpty: a row that no key reached (blocks were listed, the mask removed every key
       // of them for this row) gets O = 0 and LSE = -inf; every lane still takes part in the
       // warp-wide TMEM loads below
-      const bool none = kMask && m_ref == -CUDART_INF_F;
+      const bool none = kMayBeEmpty && m_ref == -CUDART_INF_F;
       const float inv = none ? 0.f : vsc / l_run;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -816,22 +858,29 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool make_tmap_rows128(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes) {
+bool make_tmap_rows(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes,
+                    int box_elems, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t es = static_cast<cuuint64_t>(elem_bytes);
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(T)};
   cuuint64_t strides[2] = {D * es, static_cast<cuuint64_t>(H) * D * es};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 1, 128};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_elems), 1, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType dt = elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUresult rc = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_elems * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows128(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes) {
+  return make_tmap_rows(map, base, T, H, D, elem_bytes, 128 / elem_bytes, 128);
 }
 
 namespace sm100 {
@@ -868,7 +917,8 @@ cudaError_t launch_attn_tc(const ProblemDesc& p, fpx_dtype dt, const void* q, co
                            const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                            void* o, float* lse, SeqTables t, const int32_t* order,
                            int* queue_head, const uint32_t* vbits, const uint32_t* sbits,
-                           int words, StatusBlock* st, cudaStream_t s, bool* encode_failed) {
+                           int words, const RuleDesc* rule, StatusBlock* st, cudaStream_t s,
+                           bool* encode_failed) {
   using namespace sm100;
   *encode_failed = false;
   const int64_t units = attn_tc_units(p);
@@ -883,8 +933,12 @@ cudaError_t launch_attn_tc(const ProblemDesc& p, fpx_dtype dt, const void* q, co
     return cudaErrorInvalidValue;
   }
   const bool mask = vbits != nullptr;
-  auto kern = fp8 ? (mask ? attn_tc_kernel<true, true> : attn_tc_kernel<true, false>)
-                  : (mask ? attn_tc_kernel<false, true> : attn_tc_kernel<false, false>);
+  auto kern = fp8 ? (rule   ? attn_tc_kernel<true, false, true>
+                     : mask ? attn_tc_kernel<true, true, false>
+                            : attn_tc_kernel<true, false, false>)
+                  : (rule   ? attn_tc_kernel<false, false, true>
+                     : mask ? attn_tc_kernel<false, true, false>
+                            : attn_tc_kernel<false, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
@@ -892,7 +946,7 @@ cudaError_t launch_attn_tc(const ProblemDesc& p, fpx_dtype dt, const void* q, co
   const int64_t grid = units < sm_count() ? units : sm_count();
   FPX_CHAIN(kern, static_cast<unsigned>(grid), kThreads, kSmemBytes, s, mq, mk, mv, p, row_ptr,
             col_idx, static_cast<__nv_bfloat16*>(o), lse, t, order, queue_head,
-            static_cast<int>(units), vbits, sbits, words, st);
+            static_cast<int>(units), vbits, sbits, words, rule ? *rule : RuleDesc{}, st);
   return cudaGetLastError();
 }
 

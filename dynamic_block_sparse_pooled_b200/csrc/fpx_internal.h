@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "fpx_common.cuh"
+#include "fpx_rule.cuh"
 
 namespace fpx {
 
@@ -71,6 +72,9 @@ int select_ctas(const ProblemDesc& p);
 
 // [T, H, D] tensor -> 3-D TMA map {D, H, T} with box {128 bytes, 1, 128 rows} and 128B swizzle
 // (elem_bytes 1 = u8, 2 = bf16, 4 = fp32); false if the driver rejects it.
+// make_tmap_rows: box {box_elems, 1, box_rows}, 128B swizzle (64B for boxes 64 bytes wide).
+bool make_tmap_rows(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes,
+                    int box_elems, int box_rows);
 bool make_tmap_rows128(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes);
 
 // fpx_sparse_prefill: tile schedule, then one of the two attention kernels.
@@ -83,15 +87,17 @@ cudaError_t launch_order(const ProblemDesc& p, int nb_max, SeqTables t, const in
 cudaError_t launch_attn_simt(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
                              const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                              void* o, float* lse, SeqTables t, const int32_t* order,
-                             StatusBlock* st, cudaStream_t s);
+                             const RuleDesc* rule, StatusBlock* st, cudaStream_t s);
 bool attn_tc_supported(const ProblemDesc& p, fpx_dtype dt);
 // Returns cudaSuccess or the first error; `encode_failed` is set if a tensor map was rejected.
 // vbits / sbits non-null: the vertical / slash token mask (uint32 [hq][words]) is applied.
+// rule non-null (both kernels): the score rule instead of the causal mask; CSR entries in [0, nb_s).
 cudaError_t launch_attn_tc(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
                            const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                            void* o, float* lse, SeqTables t, const int32_t* order,
                            int* queue_head, const uint32_t* vbits, const uint32_t* sbits,
-                           int words, StatusBlock* st, cudaStream_t s, bool* encode_failed);
+                           int words, const RuleDesc* rule, StatusBlock* st, cudaStream_t s,
+                           bool* encode_failed);
 
 // Query-probe vertical / slash discovery (fpx_probe.cu): zeroes and fills the two bitmasks
 // (uint32 [hq][words]).  chunk_base: [num_seqs + 1] int32; partial: float2 [total_chunks * hkv *
@@ -109,10 +115,20 @@ cudaError_t launch_vs_count(const ProblemDesc& p, SeqTables t, const uint32_t* v
                             const uint32_t* sbits, int words, uint8_t* vflag, uint8_t* sflag,
                             int32_t* counts, int64_t* cta_tot, uint32_t* mask, int mask_words,
                             cudaStream_t s);
-// The scan and emit kernels of the select stage on counts / mask written by a count kernel.
+// The scan and emit kernels of the select stage on counts / mask written by a count kernel;
+// whole_rows: blocks above the diagonal may be kept.
 cudaError_t launch_select_finish(const ProblemDesc& p, int32_t* row_ptr, int32_t* col_idx,
                                  int64_t capacity, int64_t* nnz_d, const int32_t* counts,
                                  int64_t* cta_tot, int* overflow, const uint32_t* mask,
-                                 int mask_words, SeqTables t, StatusBlock* st, cudaStream_t s);
+                                 int mask_words, SeqTables t, StatusBlock* st, cudaStream_t s,
+                                 bool whole_rows = false);
+
+// Key spans of documents (fpx_span.cu), and the blocks they reach into the select stage's keep
+// bitmask and counts (then launch_select_finish with whole_rows).
+cudaError_t launch_spans(const ProblemDesc& p, int num_docs, const int32_t* doc_cu,
+                         const int32_t* prefix, int32_t* key_lo, int32_t* key_hi, cudaStream_t s);
+cudaError_t launch_span_count(const ProblemDesc& p, const RuleDesc& rule, SeqTables t,
+                              int32_t* counts, int64_t* cta_tot, uint32_t* mask, int mask_words,
+                              cudaStream_t s);
 
 }  // namespace fpx

@@ -1,0 +1,364 @@
+// fpx_pages.cu -- the paged cache's bookkeeping on the device: block tables, the stack of free
+// pages and the slot map from request lengths (fpx_page_resize), and the write of new K / V rows
+// into the cache (fpx_kv_append).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "fpx_internal.h"
+
+namespace fpx {
+namespace pages {
+
+constexpr int kThreads = 1024;
+// tokens up to which the planning CTA writes the slot map itself; above, a second launch does
+// (a launch costs about as much as one CTA takes for this many tokens)
+constexpr int kInlineTokens = 4096;
+
+struct ResizeArgs {
+  int num_seqs, page, log2_page, num_pages, pages_per_seq, token_capacity;
+  const int32_t* lens;
+  const int32_t* new_lens;
+  const int32_t* keep;
+  int32_t* table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* cu_new;
+  int32_t* slots;
+  int32_t* positions;
+};
+
+__device__ __forceinline__ int pages_of(const ResizeArgs& a, int len) {
+  return (len + a.page - 1) >> a.log2_page;  // len <= INT32_MAX - page (checked)
+}
+
+// Pages that request s gives back (`give`), takes (`take`) and tokens it adds; false where its
+// lengths are malformed.
+struct Change {
+  int have, want, give, take, tokens, first_give;
+};
+__device__ __forceinline__ bool change_of(const ResizeArgs& a, int s, Change& c) {
+  const int n = a.lens[s], m = a.new_lens[s], keep = a.keep ? a.keep[s] : 0;
+  const int64_t most = static_cast<int64_t>(a.pages_per_seq) << a.log2_page;
+  if (n < 0 || m < 0 || n > most || m > most || keep < 0) {
+    c = {0, 0, 0, 0, 0, 0};
+    return false;
+  }
+  c.have = pages_of(a, n);
+  c.want = pages_of(a, m);
+  c.first_give = max(c.want, keep);
+  c.give = max(c.have - c.first_give, 0);
+  c.take = max(c.want - c.have, 0);
+  c.tokens = max(m - n, 0);
+  return true;
+}
+
+// Cache row of the token at position `pos` of request s: from its block table, or -1.
+__device__ __forceinline__ int slot_of(const ResizeArgs& a, int s, int pos, StatusBlock* st) {
+  const int pg = a.table[static_cast<int64_t>(s) * a.pages_per_seq + (pos >> a.log2_page)];
+  if (pg < 0 || pg >= a.num_pages) {
+    record_error(st, FPX_ERR_DEVICE_INPUT, 51, s, pg);
+    return -1;
+  }
+  return (pg << a.log2_page) + (pos & (a.page - 1));
+}
+
+__device__ __forceinline__ void write_token(const ResizeArgs& a, int t, int total,
+                                            StatusBlock* st) {
+  int slot = -1, pos = -1;
+  if (t < total) {
+    int lo = 0, hi = a.num_seqs - 1;  // largest s with cu_new[s] <= t
+    while (lo < hi) {
+      const int mid = lo + ((hi - lo + 1) >> 1);
+      if (a.cu_new[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    pos = a.lens[lo] + t - a.cu_new[lo];
+    slot = slot_of(a, lo, pos, st);
+  }
+  a.slots[t] = slot;
+  a.positions[t] = pos;
+}
+
+struct Sums {
+  int64_t give, take, tokens;
+};
+__device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
+  return {x.give + y.give, x.take + y.take, x.tokens + y.tokens};
+}
+__device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
+  return {__shfl_up_sync(0xffffffffu, x.give, o), __shfl_up_sync(0xffffffffu, x.take, o),
+          __shfl_up_sync(0xffffffffu, x.tokens, o)};
+}
+
+// One CTA: thread t owns a run of consecutive requests.  Pass 1 sums what they give, take and add;
+// a scan over the threads gives each its first place on the stack and among the tokens; the
+// totals are checked before anything is written.  Pass 2 writes cu_new and pushes the pages given
+// back; pass 3, after all pushes, pops.  The requests' lengths are read again in each pass.
+// (The stack needs the requests' order, so the scan is the operator; it is latency-bound: two
+// reads of the lengths, the scan, one page write per page moved.)
+__global__ void __launch_bounds__(kThreads) resize_kernel(ResizeArgs a, int inline_tokens,
+                                                          StatusBlock* st) {
+  pdl_enter();  // after the previous kernel on the stream
+  __shared__ Sums warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(a.num_seqs, tid * per), s1 = min(a.num_seqs, s0 + per);
+  const int count = *a.free_count;
+  Sums sum = {0, 0, 0};
+  Change c;
+  bool good = true;
+  for (int s = s0; s < s1; ++s) {
+    if (!change_of(a, s, c)) {
+      record_error(st, FPX_ERR_DEVICE_INPUT, 50, s, a.new_lens[s]);
+      good = false;
+    }
+    sum = sum + Sums{c.give, c.take, c.tokens};
+  }
+  Sums x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums y = shfl_up(x, o);
+    if (lane >= o) x = x + y;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  good = __syncthreads_and(good);
+  if (w == 0) {
+    Sums v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums y = shfl_up(v, o);
+      if (lane >= o) v = v + y;
+    }
+    warp_sum[lane] = v;
+  }
+  __syncthreads();
+  const Sums all = warp_sum[31];
+  Sums at = x;  // exclusive prefix of this thread's requests
+  if (w > 0) at = at + warp_sum[w - 1];
+  at = {at.give - sum.give, at.take - sum.take, at.tokens - sum.tokens};
+
+  const bool fits = count >= 0 && count <= a.num_pages && count + all.give <= a.num_pages &&
+                    all.take <= count + all.give && all.tokens <= a.token_capacity;
+  if (!good || !fits) {
+    if (tid == 0) {
+      if (good) record_error(st, FPX_ERR_CAPACITY, 52, count, static_cast<int>(all.take));
+      *a.free_count_out = count;
+    }
+    for (int s = tid; s <= a.num_seqs; s += kThreads) a.cu_new[s] = 0;
+    if (inline_tokens)
+      for (int t = tid; t < a.token_capacity; t += kThreads) a.slots[t] = a.positions[t] = -1;
+    return;
+  }
+  const int top = count + static_cast<int>(all.give);
+  int give = count + static_cast<int>(at.give), tok = static_cast<int>(at.tokens);
+  for (int s = s0; s < s1; ++s) {
+    change_of(a, s, c);
+    a.cu_new[s] = tok;
+    tok += c.tokens;
+    const int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.first_give;
+    for (int i = 0; i < c.give; ++i) a.free_pages[give++] = row[i];
+  }
+  const int total = static_cast<int>(all.tokens);
+  if (tid == 0) {
+    a.cu_new[a.num_seqs] = total;
+    *a.free_count_out = top - static_cast<int>(all.take);
+  }
+  __syncthreads();  // every push is on the stack, cu_new is written
+  int take = top - 1 - static_cast<int>(at.take);
+  for (int s = s0; s < s1; ++s) {
+    change_of(a, s, c);
+    int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.have;
+    for (int i = 0; i < c.take; ++i) {
+      const int pg = a.free_pages[take--];
+      if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
+      row[i] = pg;
+    }
+  }
+  if (!inline_tokens) return;
+  __syncthreads();  // the table is written
+  for (int t = tid; t < a.token_capacity; t += kThreads) write_token(a, t, total, st);
+}
+
+// The slot map of many tokens: a thread each (8 bytes written, the rest from cache).
+__global__ void __launch_bounds__(256) slots_kernel(ResizeArgs a, StatusBlock* st) {
+  pdl_enter();  // after the previous kernel on the stream
+  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  if (t < a.token_capacity) write_token(a, t, a.cu_new[a.num_seqs], st);
+}
+
+// ---- append -------------------------------------------------------------------------------------
+
+// x / scale as e4m3, round to nearest even, saturating (NaN stays NaN); the division is IEEE, so
+// the codes are those of the formula.
+__device__ __forceinline__ uint32_t quant2(float x, float y, float scale) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x, scale), __fdiv_rn(y, scale)),
+                                  __NV_SATFINITE, __NV_E4M3);
+}
+
+// A thread moves 16 bytes of source of one K or V row (blockIdx.y) at a time: rows are [hkv, d], so
+// the copy is contiguous on both sides and bound by HBM; the slot is one cached read per row.
+template <bool kQuant>
+__global__ void __launch_bounds__(256) append_kernel(
+    int64_t chunks, int row_chunks, int chunks_per_head, const char* __restrict__ k,
+    int64_t k_stride, const char* __restrict__ v, int64_t v_stride,
+    const int32_t* __restrict__ slots, char* __restrict__ k_cache, char* __restrict__ v_cache,
+    int num_slots, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+    StatusBlock* st) {
+  pdl_enter();  // after the previous kernel on the stream
+  const bool is_v = blockIdx.y != 0;
+  const char* src = is_v ? v : k;
+  const int64_t stride = is_v ? v_stride : k_stride;
+  char* dst = is_v ? v_cache : k_cache;
+  const float* scale = is_v ? v_scale : k_scale;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < chunks;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int t = static_cast<int>(i / row_chunks), c = static_cast<int>(i - static_cast<int64_t>(t) * row_chunks);
+    const int slot = slots[t];
+    if (slot < 0) continue;
+    if (slot >= num_slots) {
+      if (c == 0) record_error(st, FPX_ERR_DEVICE_INPUT, 54, t, slot);
+      continue;
+    }
+    const uint4 x = *reinterpret_cast<const uint4*>(src + t * stride + c * 16);
+    if (kQuant) {
+      const float sc = scale[c / chunks_per_head];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[j] = quant2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u), sc);
+      *reinterpret_cast<uint2*>(dst + (static_cast<int64_t>(slot) * row_chunks + c) * 8) =
+          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    } else {
+      *reinterpret_cast<uint4*>(dst + (static_cast<int64_t>(slot) * row_chunks + c) * 16) = x;
+    }
+  }
+}
+
+bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+cudaError_t launch_resize(const ResizeArgs& a, StatusBlock* st, cudaStream_t s) {
+  const bool inline_tokens = a.token_capacity <= kInlineTokens;
+  FPX_CHAIN(resize_kernel, 1, kThreads, 0, s, a, inline_tokens ? 1 : 0, st);
+  if (!inline_tokens)
+    FPX_CHAIN(slots_kernel, static_cast<unsigned>((a.token_capacity - 1) / 256 + 1), 256, 0, s, a,
+              st);
+  return cudaGetLastError();
+}
+
+template <bool kQuant>
+cudaError_t launch_append(int64_t chunks, int row_chunks, int chunks_per_head, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots,
+                          void* kc, void* vc, int num_slots, const float* ks, const float* vs,
+                          StatusBlock* st, cudaStream_t s) {
+  const int64_t want = (chunks + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(want < 148 * 16 ? want : 148 * 16);
+  FPX_CHAIN((append_kernel<kQuant>), dim3(grid, 2), 256, 0, s, chunks, row_chunks, chunks_per_head,
+            static_cast<const char*>(k), k_stride, static_cast<const char*>(v), v_stride, slots,
+            static_cast<char*>(kc), static_cast<char*>(vc), num_slots, ks, vs, st);
+  return cudaGetLastError();
+}
+
+}  // namespace pages
+}  // namespace fpx
+
+using namespace fpx;
+using fpx::pages::is_aligned;
+
+extern "C" {
+
+size_t fpx_page_workspace_bytes(int32_t num_seqs) { return num_seqs < 1 ? 0 : kStatusBytes; }
+
+fpx_status fpx_page_resize(int32_t num_seqs, int32_t page, int32_t num_pages,
+                           const int32_t* lens_d, const int32_t* new_lens_d,
+                           const int32_t* keep_pages_d, int32_t* block_table_d,
+                           int32_t pages_per_seq, int32_t* free_pages_d,
+                           const int32_t* free_count_d, int32_t* free_count_out_d,
+                           int32_t* cu_new_d, int32_t* slots_d, int32_t* positions_d,
+                           int32_t token_capacity, void* ws, size_t ws_bytes,
+                           fpx_stream_t stream) {
+  if (num_seqs < 1 || num_pages < 1 || pages_per_seq < 1 || token_capacity < 0)
+    return FPX_ERR_INVALID_ARG;
+  if (page < 16 || page > 128 || (page & (page - 1)) != 0) return FPX_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page > INT32_MAX ||
+      static_cast<int64_t>(pages_per_seq) * page > INT32_MAX - page ||
+      static_cast<int64_t>(pages_per_seq) * num_seqs > INT32_MAX)
+    return FPX_ERR_UNSUPPORTED;
+  if (!lens_d || !new_lens_d || !block_table_d || !free_pages_d || !free_count_d ||
+      !free_count_out_d || !cu_new_d || !ws)
+    return FPX_ERR_INVALID_ARG;
+  if (token_capacity > 0 && (!slots_d || !positions_d)) return FPX_ERR_INVALID_ARG;
+  const void* words[] = {lens_d,           new_lens_d, keep_pages_d, block_table_d, free_pages_d,
+                         free_count_d, free_count_out_d, cu_new_d,   slots_d,      positions_d};
+  for (const void* x : words)
+    if (!is_aligned(x, 4)) return FPX_ERR_ALIGNMENT;
+  if (!is_aligned(ws, 256)) return FPX_ERR_ALIGNMENT;
+  if (ws_bytes < fpx_page_workspace_bytes(num_seqs)) return FPX_ERR_CAPACITY;
+  pages::ResizeArgs a;
+  a.num_seqs = num_seqs;
+  a.page = page;
+  a.log2_page = 0;
+  while ((1 << a.log2_page) < page) ++a.log2_page;
+  a.num_pages = num_pages;
+  a.pages_per_seq = pages_per_seq;
+  a.token_capacity = token_capacity;
+  a.lens = lens_d;
+  a.new_lens = new_lens_d;
+  a.keep = keep_pages_d;
+  a.table = block_table_d;
+  a.free_pages = free_pages_d;
+  a.free_count = free_count_d;
+  a.free_count_out = free_count_out_d;
+  a.cu_new = cu_new_d;
+  a.slots = slots_d;
+  a.positions = positions_d;
+  return pages::launch_resize(a, static_cast<StatusBlock*>(ws),
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FPX_OK
+             : FPX_ERR_CUDA;
+}
+
+fpx_status fpx_kv_append(fpx_dtype dtype, int32_t hkv, int32_t d, int32_t num_tokens,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* slots_d, void* k_cache, void* v_cache, int32_t num_slots,
+                         const float* k_scale_d, const float* v_scale_d, void* ws,
+                         size_t ws_bytes, fpx_stream_t stream) {
+  if (dtype != FPX_F32 && dtype != FPX_BF16 && dtype != FPX_E4M3) return FPX_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FPX_ERR_UNSUPPORTED;
+  if (hkv < 1 || num_tokens < 0 || num_slots < 1) return FPX_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(hkv) * d;
+  if (row > INT32_MAX / 4) return FPX_ERR_UNSUPPORTED;
+  const bool quant = dtype == FPX_E4M3;
+  if (quant != (k_scale_d != nullptr) || quant != (v_scale_d != nullptr))
+    return FPX_ERR_INVALID_ARG;
+  if (!ws || (num_tokens > 0 && (!k || !v || !slots_d || !k_cache || !v_cache)))
+    return FPX_ERR_INVALID_ARG;
+  const int64_t es = dtype == FPX_F32 ? 4 : 2;
+  if (k_stride < row || v_stride < row || k_stride > INT64_MAX / 4 / (num_tokens + 1) ||
+      v_stride > INT64_MAX / 4 / (num_tokens + 1))
+    return FPX_ERR_INVALID_ARG;
+  if (!is_aligned(k, 16) || !is_aligned(v, 16) || (k_stride * es) % 16 != 0 ||
+      (v_stride * es) % 16 != 0 || !is_aligned(slots_d, 4) || !is_aligned(k_cache, 16) ||
+      !is_aligned(v_cache, 16) || !is_aligned(k_scale_d, 4) || !is_aligned(v_scale_d, 4) ||
+      !is_aligned(ws, 256))
+    return FPX_ERR_ALIGNMENT;
+  if (ws_bytes < kStatusBytes) return FPX_ERR_CAPACITY;
+  if (num_tokens == 0) return FPX_OK;
+  const int row_chunks = static_cast<int>(row * es / 16), per_head = static_cast<int>(d * es / 16);
+  const int64_t chunks = static_cast<int64_t>(num_tokens) * row_chunks;
+  StatusBlock* st = static_cast<StatusBlock*>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      quant ? pages::launch_append<true>(chunks, row_chunks, per_head, k, k_stride * es, v,
+                                         v_stride * es, slots_d, k_cache, v_cache, num_slots,
+                                         k_scale_d, v_scale_d, st, s)
+            : pages::launch_append<false>(chunks, row_chunks, per_head, k, k_stride * es, v,
+                                          v_stride * es, slots_d, k_cache, v_cache, num_slots,
+                                          nullptr, nullptr, st, s);
+  return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
+}
+
+}  // extern "C"

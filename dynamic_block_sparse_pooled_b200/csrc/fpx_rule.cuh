@@ -1,0 +1,67 @@
+// fpx_rule.cuh -- the score rule (cap, distance bias, key spans) as the kernels see it.
+#pragma once
+
+#include "fpx_common.cuh"
+
+namespace fpx {
+
+struct RuleDesc {
+  float softcap = 0.f;            // 0: none
+  int window = 0;                 // 0: none
+  const float* slopes = nullptr;  // [hq] or null
+  const int32_t* lo = nullptr;    // [query tokens] or null (both or neither)
+  const int32_t* hi = nullptr;
+};
+
+struct KeySpan {
+  int lo, hi;  // inclusive; lo > hi: no key
+};
+
+// Keys of a sequence of `n` tokens that the query at position i, row `tok` of Q, sees.
+__device__ __forceinline__ KeySpan rule_span(const RuleDesc& r, int64_t tok, int i, int n) {
+  KeySpan s;
+  s.lo = r.lo ? r.lo[tok] : 0;
+  s.hi = r.lo ? r.hi[tok] : i;
+  if (r.window > 0) {
+    const int64_t first = static_cast<int64_t>(i) - r.window + 1;
+    if (first > s.lo) s.lo = static_cast<int>(first);
+  }
+  if (s.lo < 0) s.lo = 0;
+  if (s.hi > n - 1) s.hi = n - 1;
+  return s;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error a few 2^-23 for any x, which is what a
+// score needs (it is scaled by the cap and then exponentiated).
+__device__ __forceinline__ float tanh_ex2(float x) {
+  return fmaf(-2.f, rcp_approx(1.f + ex2_approx(x * 2.8853900817779268f)), 1.f);
+}
+
+// Scores in log2 units from raw dot products: scale, cap, distance bias.
+struct ScoreMap {
+  float k;      // dot -> x / softcap with a cap, dot -> log2 units without
+  float cap2;   // softcap * log2 e; 0: no cap
+  float slope2; // slopes[h] * log2 e; 0: no bias
+  __device__ __forceinline__ float operator()(float dot, float dist) const {
+    float y = dot * k;
+    if (cap2 != 0.f) y = cap2 * tanh_ex2(y);
+    return fmaf(-slope2, dist, y);
+  }
+};
+
+__device__ __forceinline__ ScoreMap score_map(const RuleDesc& r, float scale, int h) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  ScoreMap m;
+  m.k = r.softcap > 0.f ? scale / r.softcap : scale * kLog2e;
+  m.cap2 = r.softcap * kLog2e;
+  m.slope2 = r.slopes ? r.slopes[h] * kLog2e : 0.f;
+  return m;
+}
+
+}  // namespace fpx

@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_emit_kernel(
     ProblemDesc p, const int32_t* __restrict__ counts, const int64_t* __restrict__ cta_off,
     int32_t* __restrict__ row_ptr, int32_t* __restrict__ col_idx,
     const int* __restrict__ overflow, const uint32_t* __restrict__ mask, int mask_words,
-    SeqTables t) {
+    int whole_rows, SeqTables t) {
   pdl_enter();  // after the previous kernel on the stream
   if (!*t.valid || *overflow) return;  // the scan published an empty CSR
   __shared__ int32_t s_off[kSelRows];
@@ -721,7 +721,8 @@ __global__ void __launch_bounds__(kSelWarps * 32) select_emit_kernel(
     if (r >= R) break;
     const RowInfo ri = row_info(p, t, r);
     const uint32_t* words = mask + static_cast<int64_t>(r) * mask_words;
-    const int nw = (ri.len + 31) >> 5;
+    // whole_rows: a row's blocks may lie above the diagonal (its unused mask words are zero)
+    const int nw = whole_rows ? mask_words : (ri.len + 31) >> 5;
     const unsigned below = (1u << lane) - 1u;
     int64_t out = base + s_off[rl];
     for (int w0 = 0; w0 < nw; w0 += 32) {  // 32 words per load, one per lane
@@ -741,7 +742,8 @@ int select_ctas(const ProblemDesc& p) { return (p.hq * p.nb_total + kSelRows - 1
 cudaError_t launch_select_finish(const ProblemDesc& p, int32_t* row_ptr, int32_t* col_idx,
                                  int64_t capacity, int64_t* nnz_d, const int32_t* counts,
                                  int64_t* cta_tot, int* overflow, const uint32_t* mask,
-                                 int mask_words, SeqTables t, StatusBlock* st, cudaStream_t s) {
+                                 int mask_words, SeqTables t, StatusBlock* st, cudaStream_t s,
+                                 bool whole_rows) {
   const int R = p.hq * p.nb_total;
   const int nblk = select_ctas(p);
   FPX_CHAIN(select_scan_kernel, 1, kScanThreads, 0, s, R, nblk, cta_tot, row_ptr, capacity, nnz_d,
@@ -749,7 +751,7 @@ cudaError_t launch_select_finish(const ProblemDesc& p, int32_t* row_ptr, int32_t
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || R == 0) return e;
   FPX_CHAIN(select_emit_kernel, nblk, kSelWarps * 32, 0, s, p, counts, cta_tot, row_ptr, col_idx,
-            overflow, mask, mask_words, t);
+            overflow, mask, mask_words, whole_rows ? 1 : 0, t);
   return cudaGetLastError();
 }
 
@@ -772,7 +774,7 @@ cudaError_t launch_select(const ProblemDesc& p, const float* scores, float alpha
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || R == 0) return e;
   FPX_CHAIN(select_emit_kernel, nblk, kSelWarps * 32, 0, s, p, counts, cta_tot, row_ptr, col_idx,
-            overflow, mask, mask_words, t);
+            overflow, mask, mask_words, 0, t);
   return cudaGetLastError();
 }
 

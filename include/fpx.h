@@ -270,6 +270,163 @@ fpx_status fpx_vs_prefill(const fpx_problem* p, const void* q, const void* k, co
                           void* ws, size_t ws_bytes, fpx_stream_t stream);
 
 /*
+ * Score rule: what a layer does to a score between the dot product and the softmax, and which keys
+ * a query sees.  With i the query's position and j the key's in their sequence (0-based):
+ *     x = scale * <q_i, k_j>
+ *     softcap > 0:  x = softcap * tanh(x / softcap)
+ *     slopes_d:     x = x - slopes[h] * |i - j|
+ *     key j is seen iff  lo_i <= j <= hi_i  and  (window == 0 or j > i - window)  and  j is a token
+ *     of the sequence;  lo = key_lo_d and hi = key_hi_d, indexed by the query token's row of Q
+ *     (NULL: lo = 0, hi = i).
+ * A query that sees no key (lo > hi, for one) gets O = 0 and LSE = -inf.  A score that is not
+ * seen may be anything, NaN included.
+ */
+typedef struct {
+  float softcap;           /* 0: none; finite, >= 0                                            */
+  int32_t window;          /* 0: none; the last `window` positions up to the query's own       */
+  const float* slopes_d;   /* device fp32 [hq], or NULL                                        */
+  const int32_t* key_lo_d; /* device int32 [query tokens], or NULL; both or neither            */
+  const int32_t* key_hi_d;
+} fpx_score_rule;
+
+/*
+ * Key spans of packed documents: for every token (position i of its sequence), with [d0, d1) the
+ * part of its document that lies in its sequence,
+ *     key_lo = d0,   key_hi = max(i, min(d0 + prefix[document], d1) - 1)
+ * as positions in the sequence: each document attends itself only, causally but for its first
+ * `prefix` tokens, which all its tokens see.
+ *   num_docs, doc_cu_d  documents as device int32 [num_docs + 1] token offsets into the packed
+ *             batch, non-decreasing; a token outside every document gets (0, -1): it sees no key.
+ *             NULL with num_docs = 0: the sequences are the documents.
+ *   prefix_d  device int32 [documents] or NULL (causal); a negative entry counts as 0.
+ *   key_lo, key_hi  device int32 [T], written.
+ */
+fpx_status fpx_spans(const fpx_problem* p, int32_t num_docs, const int32_t* doc_cu_d,
+                     const int32_t* prefix_d, int32_t* key_lo, int32_t* key_hi,
+                     fpx_stream_t stream);
+
+/*
+ * Key blocks that a rule's spans and window reach: CSR rows in fpx_select's layout; block J of row
+ * (h, s, I) is listed iff some query of block I sees a key of block J.  Unlike fpx_select's, J may
+ * be above I (a prefix seen in both directions).  Capacity rules and outputs as fpx_select (at
+ * most hq * sum nb_s^2 entries; col_capacity <= INT32_MAX); workspace: stage 1.
+ */
+fpx_status fpx_span_select(const fpx_problem* p, const fpx_score_rule* rule, int32_t* row_ptr,
+                           int32_t* col_idx, int64_t col_capacity, int64_t* nnz_d, void* ws,
+                           size_t ws_bytes, fpx_stream_t stream);
+
+/*
+ * fpx_sparse_prefill under a score rule: attention over the keys that the rule lets query i see
+ * among the blocks its CSR row lists (fpx_span_select's list covers every such key; fpx_select's
+ * drops blocks on top of the rule).  CSR entries lie in [0, nb_s); others are skipped and recorded.
+ *   kv   NULL: K and V packed; else the caches of fpx_sparse_prefill_paged (tensor-core path only).
+ * Values of V in a listed block count as multiplied by zero where they are not seen: they must be
+ * finite, as must the rows of a last page beyond the sequence.  Workspace: stage 2.
+ */
+fpx_status fpx_span_prefill(const fpx_problem* p, const void* q, const void* k, const void* v,
+                            const fpx_paged_kv* kv, const fpx_score_rule* rule,
+                            const int32_t* row_ptr, const int32_t* col_idx, void* o, float* lse,
+                            void* ws, size_t ws_bytes, fpx_stream_t stream);
+
+/*
+ * Block tables and slot maps from request lengths.  Request s grows or shrinks from lens[s] to
+ * new_lens[s] tokens; pages hold `page` tokens (power of two in [16, 128]).  In the order of s:
+ *   - a request that shrinks gives back its pages ceil(new / page) .. ceil(len / page) - 1 (those
+ *     from keep_pages[s] on, where keep_pages_d is given: the leading pages it shares with others
+ *     are not its own), pushed onto the stack free_pages[0 .. free_count) in ascending order;
+ *   - then each request that grows takes ceil(new / page) - ceil(len / page) pages from the top of
+ *     the stack into the next entries of its block-table row.
+ * Entries of the table outside a request's new pages keep their values.
+ *   lens_d, new_lens_d  device int32 [num_seqs], >= 0 and at most pages_per_seq * page.
+ *   block_table_d       device int32 [num_seqs, pages_per_seq], updated.
+ *   free_pages_d        device int32 [num_pages], the stack; entries above its new top keep theirs.
+ *   free_count_d, free_count_out_d  device int32 [1] each (may be the same): the stack's height.
+ *   cu_new_d            device int32 [num_seqs + 1]: token offsets, max(0, new - len) per request.
+ *   slots_d, positions_d  device int32 [token_capacity]: for token t of request s (the t-th added),
+ *                       at cu_new[s] + t: its cache row page_id * page + offset, and its position
+ *                       lens[s] + t.  Entries from cu_new[num_seqs] on are set to -1.
+ * lens, new_lens and the free count are only read (but where free_count_out_d is free_count_d):
+ * a call repeated on the same inputs gives the same outputs.
+ * Device-side conditions: a length that is negative or beyond the table, or keep_pages < 0:
+ * FPX_ERR_DEVICE_INPUT; too few free pages, a stack that would pass num_pages, or more tokens than
+ * token_capacity: FPX_ERR_CAPACITY.  Then nothing changes: the table and the stack keep their
+ * values, the count is copied, cu_new is all zero and slots and positions all -1.  A page id
+ * outside [0, num_pages), of the stack or the table, gives slot -1 and FPX_ERR_DEVICE_INPUT.
+ *   ws  device workspace >= fpx_page_workspace_bytes(num_seqs), also for fpx_kv_append (any size).
+ */
+size_t fpx_page_workspace_bytes(int32_t num_seqs);
+fpx_status fpx_page_resize(int32_t num_seqs, int32_t page, int32_t num_pages,
+                           const int32_t* lens_d, const int32_t* new_lens_d,
+                           const int32_t* keep_pages_d, int32_t* block_table_d,
+                           int32_t pages_per_seq, int32_t* free_pages_d,
+                           const int32_t* free_count_d, int32_t* free_count_out_d,
+                           int32_t* cu_new_d, int32_t* slots_d, int32_t* positions_d,
+                           int32_t token_capacity, void* ws, size_t ws_bytes,
+                           fpx_stream_t stream);
+
+/*
+ * Writes the K and V rows of new tokens into the paged caches: cache row slots[t] = row t, a row
+ * being [hkv, d] (d 64 or 128) values.
+ *   dtype     of the caches.  FPX_F32: fp32 rows; FPX_BF16: bf16 rows, copied; FPX_E4M3: bf16
+ *             rows, stored as e4m3(x / scale[head]), round to nearest even, saturating at +-448 (NaN stays NaN).
+ *   k, v      device, row t at k + t * k_stride elements (strides >= hkv * d; rows 16-byte aligned).
+ *   slots_d   device int32 [num_tokens]; a negative slot is skipped, one >= num_slots is skipped
+ *             and recorded as FPX_ERR_DEVICE_INPUT.  Slots must differ from one another: of two
+ *             tokens with the same slot it is not defined which values stay.
+ *   k_scale_d, v_scale_d  FPX_E4M3 only: device fp32 [hkv], > 0 (as fpx_problem's), else NULL.
+ *   num_slots rows of the caches (num_pages * page).
+ */
+fpx_status fpx_kv_append(fpx_dtype dtype, int32_t hkv, int32_t d, int32_t num_tokens,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const int32_t* slots_d, void* k_cache, void* v_cache, int32_t num_slots,
+                         const float* k_scale_d, const float* v_scale_d, void* ws,
+                         size_t ws_bytes, fpx_stream_t stream);
+
+/*
+ * Attention of each request's last q_len tokens (one when decoding; more for drafted tokens)
+ * against a paged cache that already holds them.  Query t of request s stands at position
+ * i = ctx_lens[s] - q_len + t and sees what the rule lets it see (rule NULL: keys 0 .. i); a
+ * negative position sees no key, so an unused entry of a batch has ctx_lens 0.
+ * Groups: the requests group_ptr[g] .. group_ptr[g + 1] - 1 share their first prefix_pages[g] pages
+ * (a system prompt): that part is read from the block-table row of the group's FIRST request and is
+ * loaded once for the whole group instead of once per request.  Requests of no group share
+ * nothing.  Same result as without groups, up to rounding.
+ *   q   device [num_seqs * q_len, hq, d], bf16 (FPX_BF16 and FPX_E4M3 caches) or fp32 (FPX_F32).
+ *   k_cache, v_cache  device [num_pages, page, hkv, d] in `dtype`; FPX_E4M3 values are multiplied
+ *       by k_scale / v_scale of their head.  Every row below ctx_lens must be finite unless no
+ *       query of its request sees a key within 32 positions of it; rows at and beyond ctx_lens may
+ *       hold anything.
+ *   o   device [num_seqs * q_len, hq, d] in q's type;  lse  device fp32 [hq, num_seqs * q_len] or NULL.
+ *   ctx_lens_d beyond the block table (pages_per_seq * page), or negative: FPX_ERR_DEVICE_INPUT is
+ *       recorded and it is clamped.  group_ptr that decreases or leaves [0, num_seqs], or
+ *       negative prefix_pages: FPX_ERR_DEVICE_INPUT, O = 0 and LSE = -inf everywhere.  A page
+ *       outside [0, num_pages) is recorded and read as zeros.
+ * The lengths, tables and groups are read on the device: a captured call can be replayed with others.
+ */
+typedef struct {
+  int32_t num_seqs;         /* >= 1                                                            */
+  int32_t q_len;            /* >= 1                                                            */
+  int32_t hq, hkv, d;       /* hq % hkv == 0; d 64 or 128                                      */
+  int32_t page;             /* tokens of a page: power of two in [16, 128]                     */
+  fpx_dtype dtype;          /* of the caches                                                   */
+  float softmax_scale;      /* <= 0 => 1/sqrt(d)                                               */
+  const float* k_scale_d;   /* FPX_E4M3 only: device fp32 [hkv], else NULL                     */
+  const float* v_scale_d;
+  const int32_t* ctx_lens_d;    /* device [num_seqs]                                           */
+  const int32_t* block_table_d; /* device [num_seqs, pages_per_seq]                            */
+  int32_t pages_per_seq, num_pages;
+  int32_t num_groups;           /* 0: nothing shared                                           */
+  const int32_t* group_ptr_d;   /* device [num_groups + 1], or NULL                            */
+  const int32_t* prefix_pages_d; /* device [num_groups], or NULL                               */
+} fpx_decode_problem;
+
+/* Workspace bytes of fpx_decode; 0 for an invalid problem. */
+size_t fpx_decode_workspace_bytes(const fpx_decode_problem* p);
+fpx_status fpx_decode(const fpx_decode_problem* p, const void* q, const void* k_cache,
+                      const void* v_cache, const fpx_score_rule* rule, void* o, float* lse,
+                      void* ws, size_t ws_bytes, fpx_stream_t stream);
+
+/*
  * Allocation-free variant of fpx_select (the paper has no counterpart; it exists for callers).
  *   Some callers cannot allocate device memory where they run: a plugin whose host framework
  *   owns all device memory and offers no scratch buffer, or latency-critical code that must not
