@@ -160,6 +160,17 @@ __device__ __forceinline__ float row_max64(const uint32_t* r) {
                fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
 }
 
+// Largest magnitude of 64 fp32 values.
+__device__ __forceinline__ float row_absmax64(const uint32_t* r) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 64; j += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = absmax3f(m[k], __uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // One in kPolyEvery element pairs takes exp2 on the FMA pipe instead of the MUFU (0: none).  The
 // MUFU issues four ex2 per cycle per SM sub-partition, so a 128-column row costs ~1000 cycles
 // there; moving a quarter of the pairs to the FMA pipe was measured fastest (one in two or three
@@ -171,7 +182,10 @@ constexpr int kPolyEvery = FPX_POLY_EVERY;
 
 // Columns [J0, J0 + N) of the S row in r become P, packed in place (bf16 pairs at r[J0 / 2 ..],
 // or e4m3 quads at r[J0 / 4 ..]); returns their sum.
-template <bool kFp8, int J0, int N>
+// kPoly: share the exponentials with the FMA pipe.  Under a score rule all of them stay on the MUFU:
+// the rule's own arithmetic takes the FMA pipe, and rows with few keys that count (a steep distance
+// bias) would show the polynomial's 7.5e-5 in their LSE.
+template <bool kFp8, bool kPoly, int J0, int N>
 __device__ __forceinline__ float softmax_part_to_p(uint32_t* r, float sl2, float neg_m) {
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -179,7 +193,7 @@ __device__ __forceinline__ float softmax_part_to_p(uint32_t* r, float sl2, float
     float x0, x1, p0, p1;
     ffma2(x0, x1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), sl2, sl2, neg_m, neg_m);
     constexpr int kEvery = kPolyEvery > 0 ? kPolyEvery : 1;
-    if (kPolyEvery > 0 && (j / 2) % kEvery == kEvery - 1) {
+    if (kPoly && kPolyEvery > 0 && (j / 2) % kEvery == kEvery - 1) {
       exp2_poly2(p0, p1, x0, x1);
     } else {
       p0 = ex2_approx(x0);
@@ -627,16 +641,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       ScoreMap map = {};
       KeySpan span = {0, -1};
-      bool mapped = false;
+      TanhPoly poly = {};
       if (kRule) {
         float scale = p.scale;
         if (kFp8) scale *= p.q_scale[my_h] * p.k_scale[w.kvh];
         map = score_map(rule, scale, my_h);
         if (write) span = rule_span(rule, tq, qpos, w.n_s);
         if (span.lo > span.hi) span = {0, -1};
+        poly.set(map.cap2);
         // a rule without cap and bias leaves S as it is, and the scale stays in the exponent
-        mapped = map.cap2 != 0.f || map.slope2 != 0.f;
-        sl2 = mapped ? 1.f : map.k;
+        sl2 = map.cap2 != 0.f || map.slope2 != 0.f ? 1.f : map.k;
       }
       float m_ref = -CUDART_INF_F, l_run = 0.f;
       const uint32_t* vrow = kMask ? vbits + static_cast<int64_t>(my_h) * words : nullptr;
@@ -670,10 +684,46 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // token causal mask (key column > query row) and token mask of one 64-column half
         auto mask_half = [&](uint32_t* x, int j0) {
           if (kRule) {
-            if (mapped) {
+            if (map.cap2 != 0.f) {
+              // capped scores mostly lie well within the cap, where tanh is a polynomial on the
+              // FMA pipe; a warp with a score beyond that takes 2^x and a reciprocal on the MUFU.
+              // Only seen scores count, so that no result depends on an unseen one.
+              if (partial) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j)
-                x[j] = __float_as_uint(map(__uint_as_float(x[j]), fabsf(rel - (j0 + j))));
+                for (int j = 0; j < 64; ++j)
+                  if (j0 + j < c_lo || j0 + j > c_hi) x[j] = 0u;
+              }
+              if (__all_sync(kFull, row_absmax64(x) * fabsf(map.k) <= TanhPoly::kMost)) {
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                  float x0 = __uint_as_float(x[j]), x1 = __uint_as_float(x[j + 1]);
+                  poly(x0, x1, map.k);
+                  x[j] = __float_as_uint(x0);
+                  x[j + 1] = __float_as_uint(x1);
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                  x[j] = __float_as_uint(map.cap2 * tanh_ex2(__uint_as_float(x[j]) * map.k));
+              }
+            }
+            if (map.slope2 != 0.f) {
+              // -slope |i - j| is linear in the column unless the block holds the row's diagonal
+              const float kk = map.cap2 != 0.f ? 1.f : map.k;
+              const bool before = rel >= kTileN - 1;
+              if (__all_sync(kFull, before || rel <= 0.f)) {
+                const float b1 = before ? map.slope2 : -map.slope2;
+                const float base = -b1 * rel;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                  x[j] = __float_as_uint(
+                      fmaf(__uint_as_float(x[j]), kk, fmaf(b1, static_cast<float>(j0 + j), base)));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                  x[j] = __float_as_uint(fmaf(-map.slope2, fabsf(rel - static_cast<float>(j0 + j)),
+                                              __uint_as_float(x[j]) * kk));
+              }
             }
             if (partial) {
 #pragma unroll
@@ -713,12 +763,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tmem_ld32(tS + 96, r + 96);
           mask_half(r, 0);
           const float mx_lo = row_max64(r);
-          rs = softmax_part_to_p<kFp8, 0, 64>(r, sl2, -m_ref);
+          rs = softmax_part_to_p<kFp8, !kRule, 0, 64>(r, sl2, -m_ref);
           tmem_wait_ld(r + 64);
           tmem_wait_ld(r + 96);
           mask_half(r + 64, 64);
           const float mx = fmaxf(mx_lo, row_max64(r + 64)) * sl2;
-          rs += softmax_part_to_p<kFp8, 64, 64>(r, sl2, -m_ref);
+          rs += softmax_part_to_p<kFp8, !kRule, 64, 64>(r, sl2, -m_ref);
           redo = __any_sync(kFull, mx > m_ref + kRescaleLog2);
           if (!redo) {
             if (kFp8) {
@@ -771,10 +821,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           // (a row that no key has reached yet: exponents of -inf, P = 0, and the weights the
           // FMA-pipe exp2 gives them are cleared by the rescale that its first key triggers)
           const float neg_m = (kMayBeEmpty && m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
-          rs = softmax_part_to_p<kFp8, 0, 64>(r, sl2, neg_m);
+          rs = softmax_part_to_p<kFp8, !kRule, 0, 64>(r, sl2, neg_m);
           if (kFp8) tmem_st16(tS, r);
           else tmem_st32(tS, r);
-          rs += softmax_part_to_p<kFp8, 64, 64>(r, sl2, neg_m);
+          rs += softmax_part_to_p<kFp8, !kRule, 64, 64>(r, sl2, neg_m);
           if (kFp8) tmem_st16(tS + 16, r + 16);
           else tmem_st32(tS + 32, r + 32);
         }

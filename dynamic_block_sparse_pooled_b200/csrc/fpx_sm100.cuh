@@ -218,6 +218,20 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float absmax3f(float a, float b, float c) {  // max(|a|, |b|, |c|)
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (d0, d1) = (a0, a1) * (b0, b1)
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0,
+                                      float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 // (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1) as one f32x2 instruction
 __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
                                       float c0, float c1) {
@@ -259,6 +273,31 @@ __device__ __forceinline__ void exp2_poly2(float& y0, float& y1, float x0, float
   y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
+
+// tanh(x) for |x| <= kMost on the FMA pipe: x P(x^2), P of degree 5, the coefficients minimise the
+// largest absolute error (Remez exchange; fitted by tanh_poly_fit.py; 4.220e-07 in fp32).  A factor on the
+// result is folded into the coefficients.
+struct TanhPoly {
+  static constexpr float kMost = 0.85f;
+  float c[6];
+  __device__ __forceinline__ void set(float factor) {
+    constexpr float kC[6] = {1.000000000000000e+00f, -3.333297669887543e-01f, 1.332444399595261e-01f,
+                             -5.315899476408958e-02f, 1.899728924036026e-02f, -4.207939375191927e-03f};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c[i] = kC[i] * factor;
+  }
+  // (x0, x1) = factor * tanh(k * (x0, x1)).  (k stays outside the coefficients: its 11th power
+  // would leave the range of fp32.)
+  __device__ __forceinline__ void operator()(float& x0, float& x1, float k) const {
+    float u0, u1, p0, p1;
+    fmul2(x0, x1, x0, x1, k, k);
+    fmul2(u0, u1, x0, x1, x0, x1);
+    ffma2(p0, p1, u0, u1, c[5], c[5], c[4], c[4]);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) ffma2(p0, p1, p0, p1, u0, u1, c[i], c[i]);
+    fmul2(x0, x1, x0, x1, p0, p1);
+  }
+};
 
 // ---- descriptors ------------------------------------------------------------------------
 // Shared-memory matrix descriptor (sm_100 UMMA form): start address, leading and stride byte

@@ -157,15 +157,22 @@ def test_capacity_is_recorded_and_nothing_is_written():
 
 
 def test_plain_rule_is_the_causal_attention():
-    """A rule that changes nothing gives fpx_sparse_prefill's result on a sparse CSR too."""
+    """A rule that changes nothing gives fpx_sparse_prefill's result on a sparse CSR too, up to the
+    exponentials (the rule's kernel keeps them all on the MUFU, the other shares them with a polynomial
+    of relative error 7.5e-5).  Each of the two is within (2 * 2^-8 + 2^-10) A of the exact value, A
+    the same attention of |V| (itself off by that much at most), so they are within twice that of
+    each other; their LSEs differ by the exponentials' 7.5e-5 and 32-bit roundings."""
     (q, k, v), _, _ = make("bf16", [900, 260], 4, 2, 128, gain=20.0)
     pf = fpx.problem(q, k, 128, cumulative([900, 260]))
     ws = fpx.workspace(pf, -1)
     rp, ci, _ = fpx.select(pf, fpx.block_scores(pf, q, k, ws), 0.5, ws)
     a, la = fpx.sparse_prefill(pf, q, k, v, rp, ci, ws)
     b, lb = fpx.span_prefill(pf, q, k, v, fpx.score_rule(), rp, ci, ws)
+    big, _ = fpx.sparse_prefill(pf, q, k, v.abs(), rp, ci, ws)
     assert fpx.status(ws) == 0
-    assert torch.equal(a, b) and torch.equal(la, lb)
+    rel = 2 * 2.0 ** -8 + 2.0 ** -10
+    assert ((a.double() - b.double()).abs() <= 2 * rel * (1 + rel) * big.double()).all()
+    assert (la - lb).abs().max() <= 1e-4
 
 
 def test_entries_outside_the_sequence_are_skipped_and_recorded():
