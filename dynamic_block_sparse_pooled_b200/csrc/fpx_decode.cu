@@ -146,12 +146,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeDesc p, Line o
         first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
         last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
       }
-      w.k1 = min(prefix, last);
+      // whole pages that some request's context covers: rows behind a context may hold anything
+      w.k1 = min(prefix, last & ~(p.page - 1));
       w.k0 = min(first / shared.tile * shared.tile, w.k1);
       w.tok0 = a * p.q_len;
       w.ntok = (b - a) * p.q_len;
       w.row = a;
-      w.nrt = (w.ntok * p.group + shared.rt - 1) / shared.rt;
+      w.nrt = shared.tpt ? (w.ntok + 2 * shared.tpt - 1) / (2 * shared.tpt)
+                         : (w.ntok * p.group + shared.rt - 1) / shared.rt;
     }
     if (lane == 0) shared.owners[g] = w;
   }
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeDesc p, Line o
     w.nrt = (p.q_len * p.group + own.rt - 1) / own.rt;
     if (good) {
       const int g = group_of[s];
-      const int prefix = g >= 0 ? min(p.prefix_pages[g], p.pages_per_seq) << p.log2_page : 0;
+      const int prefix = g >= 0 ? load_owner(shared.owners + g).k1 : 0;  // what the group covers
       const int lo = p.rule.window > 0 ? max(ctx - p.q_len, 0) - min(p.rule.window - 1, most) : 0;
       w.k0 = prefix + (lo > prefix ? (lo - prefix) / 32 * 32 : 0);
       w.k1 = max(ctx, w.k0);
@@ -912,26 +914,38 @@ decode_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 // ---- join -----------------------------------------------------------------------------------------
 
-// The partials of row (token, head) on one line: slots [first, first + count), row `in` of each.
+// The partials of one row on a line: `count` of them, i at slot first + i / per, row in + i % per *
+// 128 of the slot.
 struct Pieces {
   int64_t first;
-  int count, in;
+  int count, per, in;
 };
-__device__ __forceinline__ Pieces pieces_of(const Line& l, int owner, int kvh, int row) {
-  Pieces r = {0, 0, 0};
+__device__ __forceinline__ Pieces pieces_of(const Line& l, int owner, int kvh, int tok, int hg,
+                                            int group) {
+  Pieces r = {0, 0, 1, 0};
   if (owner < 0) return r;
   const Owner w = load_owner(l.owners + owner);
   const int n = tiles_of(w, l.tile);
   if (n == 0) return r;
   const int64_t total = l.owners[l.n].line;
-  const int rt = row / l.rt;
+  tok -= w.tok0;
+  int rt;
+  if (l.tpt) {
+    const int tile = tok / l.tpt;
+    rt = tile >> 1;
+    r.per = w.ntok - rt * 2 * l.tpt > l.tpt ? 1 : 2;
+    r.in = (tile & 1) * 128 + (tok - tile * l.tpt) * group + hg;
+  } else {
+    const int row = tok * group + hg;
+    rt = row / l.rt;
+    r.in = row - rt * l.rt;
+  }
   const int j = kvh * w.nrt + rt;
   const int64_t x = w.line + static_cast<int64_t>(j) * n;
   const int64_t nw = active_workers(l, total);
   const int w0 = worker_of(x, total, nw), w1 = worker_of(x + n - 1, total, nw);
   r.first = w.seg + j + w0;
-  r.count = w1 - w0 + 1;
-  r.in = row - rt * l.rt;
+  r.count = (w1 - w0 + 1) * r.per;
   return r;
 }
 
@@ -960,15 +974,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
     const int s = tok / p.q_len;
     Pieces pc[2];
     const int g = p.num_groups > 0 ? group_of[s] : -1;
-    pc[0] = g >= 0 ? pieces_of(shared, g, kvh, (tok - shared.owners[g].tok0) * p.group + hg)
-                   : Pieces{0, 0, 0};
-    pc[1] = pieces_of(own, s, kvh, (tok - s * p.q_len) * p.group + hg);
+    pc[0] = pieces_of(shared, g, kvh, tok, hg, p.group);
+    pc[1] = pieces_of(own, s, kvh, tok, hg, p.group);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Line& ln = k == 0 ? shared : own;
 #pragma unroll 4
       for (int i = sub; i < pc[k].count; i += kWpr) {
-        const int64_t at = (pc[k].first + i) * ln.rps + pc[k].in;
+        const int64_t at =
+            (pc[k].first + (pc[k].per == 2 ? i >> 1 : i)) * ln.rps + pc[k].in + (pc[k].per == 2 ? (i & 1) * 128 : 0);
         const float2 ml = ln.part_ml[at];
         float x[kVd];
         if (kVd == 4) {
@@ -1033,10 +1047,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
 
 // Warps of a worker: enough 16-row tiles for the rows that share keys, so that they are read from
 // shared memory's one copy; up to a whole CTA.
+// Rows (per group and KV head, on average) from which the shared part takes 128-row tiles.
+constexpr int kTcRows = 48;
 static int warps_for(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
 
 struct Layout {
   int rw_own, rw_shared;  // warps per worker (fp32: 1)
+  bool tc_shared;
   Line own, shared;       // offsets instead of pointers in owners / part_o / part_ml
   size_t owners_own, owners_shared, group_of, ml_own, o_own, ml_shared, o_shared, end;
 };
@@ -1056,12 +1073,15 @@ static Layout layout_of(const DecodeDesc& p, fpx_dtype dt) {
     L.shared.rt = 16 * L.rw_shared;
     L.own.tile = L.shared.tile = kTile;
   }
+  // Many rows behind a prompt: 128-row tiles on the tensor cores of the fifth generation.
+  L.tc_shared = p.num_groups > 0 && tc_supported(p, dt) && all_rows >= kTcRows * p.num_groups;
+  if (L.tc_shared) tc_line(p, &L.shared);
   L.own.n = p.num_seqs;
   L.shared.n = p.num_groups;
   L.own.nw = kCtas * (dt == FPX_F32 ? kWarpsF32 : kWarps / L.rw_own);
-  L.shared.nw = kCtas * (dt == FPX_F32 ? kWarpsF32 : kWarps / L.rw_shared);
+  L.shared.nw = L.tc_shared ? kCtas : kCtas * (dt == FPX_F32 ? kWarpsF32 : kWarps / L.rw_shared);
   L.own.rps = static_cast<int>(own_rows < L.own.rt ? own_rows : L.own.rt);
-  L.shared.rps = L.shared.rt;
+  if (!L.tc_shared) L.shared.rps = L.shared.rt;
   const size_t own_slots =
       static_cast<size_t>(p.num_seqs) * ((own_rows + L.own.rt - 1) / L.own.rt) * p.hkv + L.own.nw;
   const size_t shared_slots =
@@ -1202,9 +1222,11 @@ cudaError_t launch_decode(const decode::DecodeDesc& p, fpx_dtype dt, const void*
   }
   FPX_CHAIN(plan_kernel, 1, kPlanThreads, 0, s, p, L.own, L.shared, group_of, st);
   cudaError_t e;
-  if (p.num_groups > 0 &&
-      (e = launch_line(mk, mv, p, dt, L.shared, L.rw_shared, q, st, s)) != cudaSuccess)
-    return e;
+  if (p.num_groups > 0) {
+    e = L.tc_shared ? launch_tc(p, L.shared, q, kc, vc, st, s, encode_failed)
+                    : launch_line(mk, mv, p, dt, L.shared, L.rw_shared, q, st, s);
+    if (e != cudaSuccess) return e;
+  }
   if ((e = launch_line(mk, mv, p, dt, L.own, L.rw_own, q, st, s)) != cudaSuccess) return e;
   if (dt == FPX_F32)
     return p.d == 128 ? launch_join<float, 128>(p, L.own, L.shared, group_of, o, lse, s)

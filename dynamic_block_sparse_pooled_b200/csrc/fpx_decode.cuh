@@ -51,6 +51,10 @@ struct Line {
   int tile;  // keys of a tile
   int nw;    // workers
   int rps;   // rows stored per partial slot
+  // 0: a row tile is rt consecutive rows (token x group + head).  Else the 128-row form: tiles of
+  // tpt whole tokens, a segment has a pair of them, tile i of the pair at rows 128 i of its slot; a
+  // segment with one tile leaves two partials of it, at rows 0 and 128.
+  int tpt;
   float* part_o;    // [slots][rps][d]
   float2* part_ml;  // [slots][rps]: maximum (log2 units), sum
 };
@@ -129,9 +133,14 @@ __device__ __forceinline__ RowPos row_pos(const DecodeDesc& p, int token) {
   return r;
 }
 
+// The shared prompts on the tensor cores of the fifth generation (fpx_decode_sm100.cu).
+bool tc_supported(const DecodeDesc& p, fpx_dtype dt);
+void tc_line(const DecodeDesc& p, Line* l);  // rt, tile, rps and tpt of the 128-row form
+cudaError_t launch_tc(const DecodeDesc& p, const Line& line, const void* q, const void* kc,
+                      const void* vc, StatusBlock* st, cudaStream_t s, bool* encode_failed);
+
 }  // namespace decode
 
-// Rows of the shared prompts on the tensor cores of the fifth generation (fpx_decode_sm100.cu).
 cudaError_t launch_decode(const decode::DecodeDesc& p, fpx_dtype dt, const void* q, const void* kc,
                           const void* vc, void* o, float* lse, void* ws, StatusBlock* st,
                           cudaStream_t s, bool* encode_failed);

@@ -75,6 +75,9 @@ int select_ctas(const ProblemDesc& p);
 // make_tmap_rows: box {box_elems, 1, box_rows}, 128B swizzle (64B for boxes 64 bytes wide).
 bool make_tmap_rows(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes,
                     int box_elems, int box_rows);
+// make_tmap_heads: a bf16 [T, H, D] tensor with box {64 elements, heads, tokens}, 128B swizzle.
+bool make_tmap_heads(CUtensorMap* map, const void* base, int T, int H, int D, int heads,
+                     int tokens);
 bool make_tmap_rows128(CUtensorMap* map, const void* base, int T, int H, int D, int elem_bytes);
 
 // fpx_sparse_prefill: tile schedule, then one of the two attention kernels.

@@ -156,6 +156,57 @@ def test_shared_prompts(dtype, d, page, many):
     c.check(*fpx.decode(alone, c.qd, c.k, c.v, fpx.decode_workspace(alone)))
 
 
+PROMPTS = {
+    # name: (hq, hkv, page, requests, q_len, prompt pages, rule)
+    "two tiles": (8, 2, 128, 50, 1, 9, {}),
+    "one tile": (8, 2, 128, 30, 1, 9, {}),
+    "one key tile": (4, 1, 64, 20, 1, 1, {}),
+    "part of a key tile": (4, 1, 16, 20, 1, 13, {}),
+    "odd heads": (21, 3, 32, 37, 2, 30, {}),
+    "mqa": (64, 1, 128, 9, 1, 5, {}),
+    "mqa 128": (128, 1, 128, 3, 1, 5, {}),
+    "mha": (4, 4, 128, 300, 1, 3, {}),
+    "window": (8, 2, 64, 40, 3, 20, dict(window=700)),
+    "window behind": (8, 2, 64, 40, 1, 20, dict(window=5)),
+    "cap": (8, 2, 128, 50, 1, 9, dict(softcap=6.0)),
+    "cap far": (8, 2, 128, 30, 1, 9, dict(softcap=0.5)),
+    "bias": (8, 2, 32, 50, 1, 9, dict(slopes=True)),
+    "cap bias window": (6, 2, 16, 45, 2, 70, dict(softcap=9.0, slopes=True, window=900)),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("name", sorted(PROMPTS))
+def test_many_rows_behind_a_prompt(dtype, name):
+    hq, hkv, page, n, q_len, pages, rule = PROMPTS[name]
+    pre = pages * page
+    ctx = [pre + q_len + (5 * i) % 90 for i in range(n)]
+    ctx[1], ctx[2] = 0, max(pre - 7, 0)  # an unused entry, one that ends inside the prompt
+    c = Case(dtype, ctx, hq, hkv, 128, page, q_len, groups=[0, n], prefix=[pages], seed=14)
+    kw = dict(rule)
+    if kw.get("slopes"):
+        kw["slopes"] = torch.pow(2.0, -8.0 * torch.arange(1, hq + 1).double() / hq).float()
+    dev = dict(kw)
+    if dev.get("slopes") is not None:
+        dev["slopes"] = dev["slopes"].cuda()
+    out = c.run(fpx.score_rule(**dev))
+    c.check(*out, **kw)
+    assert fpx.status(c.ws) == 0
+    again = c.run(fpx.score_rule(**dev))
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
+def test_prompts_beyond_every_context():
+    """All contexts end inside the shared pages; what lies behind them is garbage."""
+    c = Case("bf16", [100, 77, 0, 33] * 8, 8, 2, 128, 32, groups=[0, 32], prefix=[4], seed=15)
+    keep = torch.tensor([100, 77, 0, 33] * 8)
+    for s in range(0, 32):  # rows of the prompt's last page behind the longest context
+        pg = int(c.table[s, 3])
+        c.k[pg, 4:], c.v[pg, 4:] = float("nan"), float("nan")
+    c.check(*c.run())
+    assert keep.max() == 100 and fpx.status(c.ws) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_group_of_empty_requests(dtype):
     c = Case(dtype, [0, 0, 40], 4, 1, 128, 16, groups=[0, 2], prefix=[2], seed=6)
