@@ -494,41 +494,36 @@ def vs_path(q, k, v, block: int, n_probe: int, alpha_v: float, alpha_s: float, c
 
 # ---- attention under a score rule -----------------------------------------------------------
 
-def _expect(name: str, t: Optional[torch.Tensor], dtype, device=None, numel: int = 0,
+def _expect(name: str, t: Optional[torch.Tensor], dtype, device: int = -2, numel: int = 0,
             shape=None) -> None:
-    """Refuses a tensor that the device code would misread (None passes)."""
+    """Refuses a tensor that the device code would misread (None passes; device: its index)."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if device != -2 and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected device {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} entries, needs {numel}")
 
 
-class _On:
-    """Launches go to `device`: makes it current if it is not; the stream defaults to its own."""
-
-    def __init__(self, device, stream):
-        self.index = device.index if device.index is not None else torch.cuda.current_device()
-        self.stream = stream
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.index)
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
-        return False
+def _call(name: str, device: int, stream, *args) -> None:
+    """Calls entry point `name` with the stream as its last argument (default: the device's current
+    one) and the device current."""
+    fn = getattr(_lib or load(), name)
+    handle = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, handle)
+    if code != 0:
+        raise FpxError(code, name)
 
 
 def score_rule(softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
@@ -547,8 +542,8 @@ def score_rule(softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, wind
     return r
 
 
-def _check_rule(rule: ScoreRule, hq: int, tokens: int, device) -> None:
-    slopes, lo, hi = getattr(rule, "_keep", (None, None, None))
+def _check_rule(rule: ScoreRule, hq: int, tokens: int, device: int) -> None:
+    slopes, lo, hi = rule._keep
     _expect("slopes", slopes, torch.float32, device, hq)
     _expect("key_lo", lo, torch.int32, device, tokens)
     _expect("key_hi", hi, torch.int32, device, tokens)
@@ -561,20 +556,20 @@ def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
     offsets; None: each sequence) attends itself, causally but for its first prefix[document]
     tokens.  `device` is needed only where no tensor names one."""
     given = [t for t in (key_lo, key_hi, doc_cu, prefix, pf.cu_d) if t is not None]
-    dev = given[0].device if given else torch.device(device or "cuda")
+    on = given[0].device if given else torch.device(device or "cuda")
+    dev = on.index if on.index is not None else torch.cuda.current_device()
     total = pf.struct.total_tokens
     docs = 0 if doc_cu is None else doc_cu.numel() - 1
     if doc_cu is not None and docs < 1:
         raise ValueError("doc_cu needs at least one document")
     _expect("doc_cu", doc_cu, torch.int32, dev)
     _expect("prefix", prefix, torch.int32, dev, docs if doc_cu is not None else pf.struct.num_seqs)
-    key_lo = torch.empty(total, dtype=torch.int32, device=dev) if key_lo is None else key_lo
-    key_hi = torch.empty(total, dtype=torch.int32, device=dev) if key_hi is None else key_hi
+    key_lo = torch.empty(total, dtype=torch.int32, device=on) if key_lo is None else key_lo
+    key_hi = torch.empty(total, dtype=torch.int32, device=on) if key_hi is None else key_hi
     _expect("key_lo", key_lo, torch.int32, dev, total)
     _expect("key_hi", key_hi, torch.int32, dev, total)
-    with _On(dev, stream) as s:
-        check(load().fpx_spans(pf.ptr, docs, _ptr(doc_cu), _ptr(prefix), _ptr(key_lo),
-                               _ptr(key_hi), s), "fpx_spans")
+    _call("fpx_spans", dev, stream, pf.ptr, docs, _ptr(doc_cu), _ptr(prefix), _ptr(key_lo),
+          _ptr(key_hi))
     return key_lo, key_hi
 
 
@@ -589,8 +584,8 @@ def span_capacity(pf: Prefill) -> int:
 def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, col_idx=None,
                 nnz=None, capacity: Optional[int] = None, stream=None):
     """fpx_span_select -> (row_ptr, col_idx, nnz): the key blocks that the rule's spans reach."""
-    dev = ws.device
-    _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, dev)
+    dev, index = ws.device, ws.get_device()
+    _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, index)
     if row_ptr is None:
         row_ptr = torch.empty(pf.rows + 1, dtype=torch.int32, device=dev)
     if col_idx is None:
@@ -600,9 +595,8 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
     if nnz is None:
         nnz = torch.empty(1, dtype=torch.int64, device=dev)
     _check_csr_outputs(pf, row_ptr, col_idx, nnz, cap)
-    with _On(dev, stream) as s:
-        check(load().fpx_span_select(pf.ptr, ctypes.byref(rule), _ptr(row_ptr), _ptr(col_idx), cap,
-                                     _ptr(nnz), _ptr(ws), ws.numel(), s), "fpx_span_select")
+    _call("fpx_span_select", index, stream, pf.ptr, ctypes.byref(rule), _ptr(row_ptr),
+          _ptr(col_idx), cap, _ptr(nnz), _ptr(ws), ws.numel())
     return row_ptr, col_idx, nnz
 
 
@@ -612,7 +606,7 @@ def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                  lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
     """fpx_span_prefill -> (O, LSE): attention over the listed blocks under the rule.  K and V are
     packed, or with `kv` the page caches."""
-    p, dev = pf.struct, q.device
+    p, dev = pf.struct, q.get_device()
     _expect("q", q, q.dtype, dev, shape=(p.total_tokens, p.hq, p.d))
     rows = kv.num_pages * p.block if kv is not None else p.total_tokens
     for name, t in (("k", k), ("v", v)):
@@ -625,16 +619,14 @@ def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _expect("row_ptr", row_ptr, torch.int32, dev, pf.rows + 1)
     _expect("col_idx", col_idx, torch.int32, dev)
     odt = torch.float32 if q.dtype == torch.float32 else torch.bfloat16
-    o = torch.empty(q.shape, dtype=odt, device=dev) if o is None else o
+    o = torch.empty(q.shape, dtype=odt, device=q.device) if o is None else o
     if lse is None and want_lse:
-        lse = torch.empty((p.hq, p.total_tokens), dtype=torch.float32, device=dev)
+        lse = torch.empty((p.hq, p.total_tokens), dtype=torch.float32, device=q.device)
     _expect("o", o, odt, dev, shape=q.shape)
     _expect("lse", lse, torch.float32, dev, p.hq * p.total_tokens)
-    with _On(dev, stream) as s:
-        check(load().fpx_span_prefill(pf.ptr, _ptr(q), _ptr(k), _ptr(v),
-                                      ctypes.byref(kv) if kv is not None else None,
-                                      ctypes.byref(rule), _ptr(row_ptr), _ptr(col_idx), _ptr(o),
-                                      _ptr(lse), _ptr(ws), ws.numel(), s), "fpx_span_prefill")
+    _call("fpx_span_prefill", dev, stream, pf.ptr, _ptr(q), _ptr(k), _ptr(v),
+          ctypes.byref(kv) if kv is not None else None, ctypes.byref(rule), _ptr(row_ptr),
+          _ptr(col_idx), _ptr(o), _ptr(lse), _ptr(ws), ws.numel())
     return o, lse
 
 
@@ -643,7 +635,7 @@ def span_path(q, k, v, block: int, cu_seqlens=None, doc_cu=None, prefix=None, so
               v_scale=None, stream=None) -> dict:
     """The whole path under a rule on one stream: spans -> blocks -> O, LSE.  Raises on any
     recorded error."""
-    with _On(q.device, stream):
+    with torch.cuda.device(q.device):
         if stream is None:
             stream = torch.cuda.current_stream(q.device)
         pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
@@ -673,34 +665,36 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     """fpx_page_resize: requests grow or shrink from lens to new_lens -> (cu_new int32 [S + 1],
     slots int32 [token_capacity], positions int32 [token_capacity]).  block_table, free_pages and
     the count (count_out, by default free_count itself) are updated."""
-    dev, n = lens.device, lens.numel()
+    dev, n = lens.get_device(), lens.numel()
     count_out = free_count if count_out is None else count_out
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table must be [num_seqs, pages_per_seq]")
-    for name, t, need in (("lens", lens, n), ("new_lens", new_lens, n),
-                          ("keep_pages", keep_pages, n), ("block_table", block_table, 0),
-                          ("free_pages", free_pages, num_pages), ("free_count", free_count, 1),
-                          ("count_out", count_out, 1)):
-        _expect(name, t, torch.int32, dev, need)
-    cu_new = torch.empty(n + 1, dtype=torch.int32, device=dev) if cu_new is None else cu_new
+    on = lens.device
+    if cu_new is None:
+        cu_new = torch.empty(n + 1, dtype=torch.int32, device=on)
     if slots is None:
-        slots = torch.empty(token_capacity, dtype=torch.int32, device=dev)
+        slots = torch.empty(token_capacity, dtype=torch.int32, device=on)
     if positions is None:
-        positions = torch.empty(token_capacity, dtype=torch.int32, device=dev)
-    for name, t, need in (("cu_new", cu_new, n + 1), ("slots", slots, token_capacity),
-                          ("positions", positions, token_capacity)):
-        _expect(name, t, torch.int32, dev, need)
-    with _On(dev, stream) as s:
-        check(load().fpx_page_resize(n, int(page), int(num_pages), _ptr(lens), _ptr(new_lens),
-                                     _ptr(keep_pages), _ptr(block_table), block_table.shape[1],
-                                     _ptr(free_pages), _ptr(free_count), _ptr(count_out),
-                                     _ptr(cu_new), _ptr(slots), _ptr(positions),
-                                     int(token_capacity), _ptr(ws), ws.numel(), s),
-              "fpx_page_resize")
+        positions = torch.empty(token_capacity, dtype=torch.int32, device=on)
+    i32 = torch.int32
+    _expect("lens", lens, i32, dev)
+    _expect("new_lens", new_lens, i32, dev, n)
+    _expect("keep_pages", keep_pages, i32, dev, n)
+    _expect("block_table", block_table, i32, dev)
+    _expect("free_pages", free_pages, i32, dev, num_pages)
+    _expect("free_count", free_count, i32, dev, 1)
+    _expect("count_out", count_out, i32, dev, 1)
+    _expect("cu_new", cu_new, i32, dev, n + 1)
+    _expect("slots", slots, i32, dev, token_capacity)
+    _expect("positions", positions, i32, dev, token_capacity)
+    _call("fpx_page_resize", dev, stream, n, page, num_pages, lens.data_ptr(),
+          new_lens.data_ptr(), _ptr(keep_pages), block_table.data_ptr(), block_table.shape[1],
+          free_pages.data_ptr(), free_count.data_ptr(), count_out.data_ptr(), cu_new.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), token_capacity, ws.data_ptr(), ws.numel())
     return cu_new, slots, positions
 
 
-def _cache_rows(name: str, t: torch.Tensor, hkv: int, d: int, device) -> int:
+def _cache_rows(name: str, t: torch.Tensor, hkv: int, d: int, device: int) -> int:
     if t.dim() < 3 or t.shape[-1] != d or t.shape[-2] != hkv:
         raise ValueError(f"{name} must be [.., {hkv}, {d}], got {tuple(t.shape)}")
     _expect(name, t, t.dtype, device)
@@ -713,26 +707,27 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: to
     """fpx_kv_append: rows k, v [n, Hkv, D] (each row contiguous; the rows may be strided, as slices
     of a projection's output are) into cache rows slots[n].  e4m3 caches take bf16 rows and the
     heads' scales (fp32 [Hkv])."""
-    dev, (n, hkv, d) = k.device, k.shape
+    dev, (n, hkv, d) = k.get_device(), k.shape
     if k_cache.dtype not in _DTYPES:
         raise TypeError(f"unsupported cache type {k_cache.dtype}")
-    src = torch.float32 if k_cache.dtype == torch.float32 else torch.bfloat16
+    src = torch.float32 if k_cache.dtype is torch.float32 else torch.bfloat16
+    strides = []
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != src or t.device != dev or tuple(t.shape) != (n, hkv, d):
-            raise ValueError(f"{name} must be {src} {(n, hkv, d)} on {dev}")
-        if n > 0 and (t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d)):
+        if t.dtype is not src or t.get_device() != dev or t.shape != k.shape:
+            raise ValueError(f"{name} must be {src} {(n, hkv, d)} on device {dev}")
+        step, head, one = t.stride()
+        if n > 0 and (one != 1 or (hkv > 1 and head != d)):
             raise ValueError(f"a row of {name} must be contiguous")
+        strides.append(step if n > 1 else hkv * d)
     rows = _cache_rows("k_cache", k_cache, hkv, d, dev)
-    if _cache_rows("v_cache", v_cache, hkv, d, dev) != rows or v_cache.dtype != k_cache.dtype:
+    if _cache_rows("v_cache", v_cache, hkv, d, dev) != rows or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache and v_cache must have the same rows and type")
     _expect("slots", slots, torch.int32, dev, n)
     _expect("k_scale", k_scale, torch.float32, dev, hkv)
     _expect("v_scale", v_scale, torch.float32, dev, hkv)
-    ks, vs = (t.stride(0) if n > 1 else hkv * d for t in (k, v))
-    with _On(dev, stream) as s:
-        check(load().fpx_kv_append(_DTYPES[k_cache.dtype], hkv, d, n, _ptr(k), ks, _ptr(v), vs,
-                                   _ptr(slots), _ptr(k_cache), _ptr(v_cache), rows, _ptr(k_scale),
-                                   _ptr(v_scale), _ptr(ws), ws.numel(), s), "fpx_kv_append")
+    _call("fpx_kv_append", dev, stream, _DTYPES[k_cache.dtype], hkv, d, n, k.data_ptr(),
+          strides[0], v.data_ptr(), strides[1], slots.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), rows, _ptr(k_scale), _ptr(v_scale), ws.data_ptr(), ws.numel())
 
 
 @dataclass
@@ -740,7 +735,7 @@ class Decode:
     """One decode problem bound to device tensors (keeps them and the struct alive)."""
     struct: DecodeProblem
     keep: tuple
-    q_shape: tuple
+    q_shape: torch.Size
     q_dtype: torch.dtype
     device: torch.device
 
@@ -761,7 +756,7 @@ def decode_problem(q: torch.Tensor, k_cache: torch.Tensor, ctx_lens: torch.Tenso
         raise TypeError(f"unsupported cache type {k_cache.dtype}")
     if k_cache.dim() != 4 or q.dim() != 3:
         raise ValueError("k_cache must be [num_pages, page, Hkv, D] and q [tokens, Hq, D]")
-    dev, n = q.device, ctx_lens.numel()
+    dev, n = q.get_device(), ctx_lens.numel()
     num_pages, page, hkv, d = k_cache.shape
     if q.shape[0] != n * q_len or q.shape[2] != d:
         raise ValueError(f"q must be [{n} * {q_len}, Hq, {d}], got {tuple(q.shape)}")
@@ -785,7 +780,7 @@ def decode_problem(q: torch.Tensor, k_cache: torch.Tensor, ctx_lens: torch.Tenso
                       _ptr(prefix_pages))
     qdt = torch.float32 if k_cache.dtype == torch.float32 else torch.bfloat16
     return Decode(s, (ctx_lens, block_table, k_scale, v_scale, group_ptr, prefix_pages),
-                  tuple(q.shape), qdt, dev)
+                  q.shape, qdt, q.device)
 
 
 def decode_workspace(dp: Decode) -> torch.Tensor:
@@ -800,7 +795,7 @@ def decode(dp: Decode, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
            ws: torch.Tensor, rule: Optional[ScoreRule] = None, o: Optional[torch.Tensor] = None,
            lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
     """fpx_decode -> (O [S * q_len, Hq, D], LSE fp32 [Hq, S * q_len])."""
-    p, dev = dp.struct, dp.device
+    p, dev = dp.struct, dp.keep[0].get_device()
     tokens = dp.q_shape[0]
     _expect("q", q, dp.q_dtype, dev, shape=dp.q_shape)
     shape = (p.num_pages, p.page, p.hkv, p.d)
@@ -810,13 +805,15 @@ def decode(dp: Decode, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         _expect(name, t, t.dtype, dev, shape=shape)
     if rule is not None:
         _check_rule(rule, p.hq, tokens, dev)
-    o = torch.empty(dp.q_shape, dtype=dp.q_dtype, device=dev) if o is None else o
-    if lse is None and want_lse:
-        lse = torch.empty((p.hq, tokens), dtype=torch.float32, device=dev)
-    _expect("o", o, dp.q_dtype, dev, shape=dp.q_shape)
-    _expect("lse", lse, torch.float32, dev, p.hq * tokens)
-    with _On(dev, stream) as s:
-        check(load().fpx_decode(dp.ptr, _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                ctypes.byref(rule) if rule is not None else None, _ptr(o),
-                                _ptr(lse), _ptr(ws), ws.numel(), s), "fpx_decode")
+    if o is None:
+        o = torch.empty(dp.q_shape, dtype=dp.q_dtype, device=dp.device)
+    else:
+        _expect("o", o, dp.q_dtype, dev, shape=dp.q_shape)
+    if lse is not None:
+        _expect("lse", lse, torch.float32, dev, p.hq * tokens)
+    elif want_lse:
+        lse = torch.empty((p.hq, tokens), dtype=torch.float32, device=dp.device)
+    _call("fpx_decode", dev, stream, dp.ptr, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          ctypes.byref(rule) if rule is not None else None, o.data_ptr(), _ptr(lse),
+          ws.data_ptr(), ws.numel())
     return o, lse

@@ -496,10 +496,10 @@ static fpx_status sparse_prefill_impl(const fpx_problem* p, const void* q, const
     if (encode_failed) return FPX_ERR_UNSUPPORTED;
     return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
   }
-  return launch_attn_simt(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order,
-                          rule ? &rd : nullptr, st, s) == cudaSuccess
-             ? FPX_OK
-             : FPX_ERR_CUDA;
+  const cudaError_t e =
+      rule ? launch_span_simt(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order, rd, st, s)
+           : launch_attn_simt(d, p->dtype, q, k, v, row_ptr, col_idx, o, lse, t, order, st, s);
+  return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
 }
 
 fpx_status fpx_sparse_prefill(const fpx_problem* p, const void* q, const void* k, const void* v,

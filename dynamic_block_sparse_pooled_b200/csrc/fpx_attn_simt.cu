@@ -36,14 +36,11 @@ __device__ __forceinline__ void store_val<__nv_bfloat16>(__nv_bfloat16* p, float
   *p = __float2bfloat16_rn(x);
 }
 
-// kRule: the score rule replaces the causal mask (scores cap and bias, key spans, CSR entries
-// above the diagonal).
-template <typename T, typename OT, int D, bool kRule>
+template <typename T, typename OT, int D>
 __global__ void __launch_bounds__(256) attn_simt_kernel(
     ProblemDesc p, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ col_idx, OT* __restrict__ o,
-    float* __restrict__ lse, SeqTables t, const int32_t* __restrict__ order, RuleDesc rule,
-    StatusBlock* st) {
+    float* __restrict__ lse, SeqTables t, const int32_t* __restrict__ order, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
   constexpr int TPR = D / 64;  // threads per query row
   __shared__ float sk[kSimtChunk][D + 1];
@@ -68,18 +65,11 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(
   const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
   const float sl2 = p.scale * qs * ks * 1.4426950408889634f;  // logits in log2 units
 
-  ScoreMap map = {};
-  KeySpan span = {1, 0};
-  if (kRule) {
-    map = score_map(rule, p.scale * qs * ks, h);
-    if (valid) span = rule_span(rule, tok0 + qpos, qpos, n_s);
-  }
-
   float qv[64], acc[64];
   const T* qrow = q + ((tok0 + (valid ? qpos : 0)) * p.hq + h) * D + part * 64;
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    qv[i] = valid ? load_val(qrow + i) * (kRule ? 1.f : sl2) : 0.f;
+    qv[i] = valid ? load_val(qrow + i) * sl2 : 0.f;
     acc[i] = 0.f;
   }
   float m = -CUDART_INF_F, l = 0.f;
@@ -87,7 +77,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(
   const int beg = row_ptr[r], end = row_ptr[r + 1];
   for (int e = beg; e < end; ++e) {
     const int J = col_idx[e];
-    if (J < 0 || J > (kRule ? (n_s - 1) / p.block : I)) {
+    if (J < 0 || J > I) {
       if (threadIdx.x == 0) record_error(st, FPX_ERR_DEVICE_INPUT, 20, r, J);
       continue;
     }
@@ -114,12 +104,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(
 #pragma unroll
         for (int i = 0; i < 64; ++i) dot = fmaf(qv[i], sk[c][part * 64 + i], dot);
         if (TPR == 2) dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-        bool ok = c < nk && (c0 + c) <= qpos;
-        if (kRule) {
-          const int j = c0 + c;
-          dot = map(dot, static_cast<float>(abs(qpos - j)));
-          ok = c < nk && j >= span.lo && j <= span.hi;
-        }
+        const bool ok = c < nk && (c0 + c) <= qpos;
         sc[c] = ok ? dot : -CUDART_INF_F;
         cmax = fmaxf(cmax, sc[c]);
       }
@@ -150,50 +135,39 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(
         l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
-template <typename T, typename OT, bool kRule>
+template <typename T, typename OT>
 static cudaError_t launch_simt_t(const ProblemDesc& p, const void* q, const void* k,
                                  const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                                  void* o, float* lse, SeqTables t, const int32_t* order,
-                                 const RuleDesc& rule, StatusBlock* st, cudaStream_t s) {
+                                 StatusBlock* st, cudaStream_t s) {
   const int R = p.hq * p.nb_total;
   const int threads = p.block * (p.d / 64);
   if (p.d == 128)
-    FPX_CHAIN((attn_simt_kernel<T, OT, 128, kRule>), R, threads, 0, s, p, static_cast<const T*>(q),
+    FPX_CHAIN((attn_simt_kernel<T, OT, 128>), R, threads, 0, s, p, static_cast<const T*>(q),
               static_cast<const T*>(k), static_cast<const T*>(v), row_ptr, col_idx,
-              static_cast<OT*>(o), lse, t, order, rule, st);
+              static_cast<OT*>(o), lse, t, order, st);
   else
-    FPX_CHAIN((attn_simt_kernel<T, OT, 64, kRule>), R, threads, 0, s, p, static_cast<const T*>(q),
+    FPX_CHAIN((attn_simt_kernel<T, OT, 64>), R, threads, 0, s, p, static_cast<const T*>(q),
               static_cast<const T*>(k), static_cast<const T*>(v), row_ptr, col_idx,
-              static_cast<OT*>(o), lse, t, order, rule, st);
+              static_cast<OT*>(o), lse, t, order, st);
   return cudaGetLastError();
-}
-
-template <bool kRule>
-static cudaError_t launch_simt_r(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
-                                 const void* v, const int32_t* row_ptr, const int32_t* col_idx,
-                                 void* o, float* lse, SeqTables t, const int32_t* order,
-                                 const RuleDesc& rule, StatusBlock* st, cudaStream_t s) {
-  switch (dt) {
-    case FPX_F32:
-      return launch_simt_t<float, float, kRule>(p, q, k, v, row_ptr, col_idx, o, lse, t, order,
-                                                rule, st, s);
-    case FPX_BF16:
-      return launch_simt_t<__nv_bfloat16, __nv_bfloat16, kRule>(p, q, k, v, row_ptr, col_idx, o,
-                                                                lse, t, order, rule, st, s);
-    default:
-      return launch_simt_t<__nv_fp8_e4m3, __nv_bfloat16, kRule>(p, q, k, v, row_ptr, col_idx, o,
-                                                                lse, t, order, rule, st, s);
-  }
 }
 
 cudaError_t launch_attn_simt(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
                              const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                              void* o, float* lse, SeqTables t, const int32_t* order,
-                             const RuleDesc* rule, StatusBlock* st, cudaStream_t s) {
+                             StatusBlock* st, cudaStream_t s) {
   if (p.hq * p.nb_total == 0) return cudaSuccess;
-  return rule ? launch_simt_r<true>(p, dt, q, k, v, row_ptr, col_idx, o, lse, t, order, *rule, st, s)
-              : launch_simt_r<false>(p, dt, q, k, v, row_ptr, col_idx, o, lse, t, order, RuleDesc{},
-                                     st, s);
+  switch (dt) {
+    case FPX_F32:
+      return launch_simt_t<float, float>(p, q, k, v, row_ptr, col_idx, o, lse, t, order, st, s);
+    case FPX_BF16:
+      return launch_simt_t<__nv_bfloat16, __nv_bfloat16>(p, q, k, v, row_ptr, col_idx, o, lse,
+                                                         t, order, st, s);
+    default:
+      return launch_simt_t<__nv_fp8_e4m3, __nv_bfloat16>(p, q, k, v, row_ptr, col_idx, o, lse,
+                                                         t, order, st, s);
+  }
 }
 
 }  // namespace fpx

@@ -90,11 +90,11 @@ cudaError_t launch_order(const ProblemDesc& p, int nb_max, SeqTables t, const in
 cudaError_t launch_attn_simt(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
                              const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                              void* o, float* lse, SeqTables t, const int32_t* order,
-                             const RuleDesc* rule, StatusBlock* st, cudaStream_t s);
+                             StatusBlock* st, cudaStream_t s);
 bool attn_tc_supported(const ProblemDesc& p, fpx_dtype dt);
 // Returns cudaSuccess or the first error; `encode_failed` is set if a tensor map was rejected.
 // vbits / sbits non-null: the vertical / slash token mask (uint32 [hq][words]) is applied.
-// rule non-null (both kernels): the score rule instead of the causal mask; CSR entries in [0, nb_s).
+// rule non-null: the score rule instead of the causal mask; CSR entries in [0, nb_s).
 cudaError_t launch_attn_tc(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
                            const void* v, const int32_t* row_ptr, const int32_t* col_idx,
                            void* o, float* lse, SeqTables t, const int32_t* order,
@@ -130,6 +130,11 @@ cudaError_t launch_select_finish(const ProblemDesc& p, int32_t* row_ptr, int32_t
 // bitmask and counts (then launch_select_finish with whole_rows).
 cudaError_t launch_spans(const ProblemDesc& p, int num_docs, const int32_t* doc_cu,
                          const int32_t* prefix, int32_t* key_lo, int32_t* key_hi, cudaStream_t s);
+// fpx_span_prefill on the CUDA cores (fpx_span_simt.cu).
+cudaError_t launch_span_simt(const ProblemDesc& p, fpx_dtype dt, const void* q, const void* k,
+                             const void* v, const int32_t* row_ptr, const int32_t* col_idx, void* o,
+                             float* lse, SeqTables t, const int32_t* order, const RuleDesc& rule,
+                             StatusBlock* st, cudaStream_t s);
 cudaError_t launch_span_count(const ProblemDesc& p, const RuleDesc& rule, SeqTables t,
                               int32_t* counts, int64_t* cta_tot, uint32_t* mask, int mask_words,
                               cudaStream_t s);
