@@ -23,6 +23,7 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstdint>
 
@@ -299,13 +300,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ void sts128_zero(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
-// Two e4m3 codes (low half of x) to f16x2; exact.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(y)
+// Four e4m3 codes to two f16x2 (codes 0, 1 and codes 2, 3); exact.
+__device__ __forceinline__ void f16x2_of_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(x));
-  return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
@@ -411,6 +411,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     return true;
   };
 
+  const bool capped = p.rule.softcap > 0.f, biased = p.rule.slopes != nullptr;
   Cursor cur;
   cur.seek(line, x0);
   int left = x1 - x0;
@@ -428,6 +429,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     ScoreMap map[2];
     bool valid[2];
     uint32_t qf[kSteps][4];
+    float mul[2];
     float kscale = p.scale;
     if (kFp8) kscale *= p.k_scale[kvh];
 #pragma unroll
@@ -480,6 +482,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
       }
       map[h] = score_map(p.rule, kscale * row_scale, head[h]);
+      // without cap and bias the scale stays in the exponent (kept above 0: -inf * 0 is NaN)
+      mul[h] = capped || biased ? 1.f : fmaxf(map[h].k, FLT_MIN);
     }
     float acc[D / 8][4];
 #pragma unroll
@@ -509,9 +513,11 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               const uint4 u = lds128(kt + swz<H::kRowB>(key, hf * 4 + c4));
               const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma16816<true>(s[nt], qf[hf * 4 + i], f16x2_of_e4m3(w4[i]),
-                               f16x2_of_e4m3(w4[i] >> 16));
+              for (int i = 0; i < 4; ++i) {
+                uint32_t b0, b1;
+                f16x2_of_e4m3(w4[i], b0, b1);
+                mma16816<true>(s[nt], qf[hf * 4 + i], b0, b1);
+              }
             }
           }
         } else {
@@ -536,17 +542,35 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (active) {
         const bool partial = __any_sync(kFull, span[0].lo > kb || span[0].hi < kb + kTile - 1 ||
                                                    span[1].lo > kb || span[1].hi < kb + kTile - 1);
+        if (capped) {
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+          for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int h = k >> 1;
-            const int col = c4 * 2 + (k & 1);
-            const int key = kb + nt * 8 + (kFp8 ? key_of_col(col) : col);
-            float y = map[h](s[nt][k], fabsf(static_cast<float>(pos[h] - key)));
-            if (partial && (key < span[h].lo || key > span[h].hi)) y = -CUDART_INF_F;
-            s[nt][k] = y;
-          }
+            for (int k = 0; k < 4; ++k)
+              s[nt][k] = map[k >> 1].cap2 * tanh_ex2(s[nt][k] * map[k >> 1].k);
+        }
+        if (biased) {
+          const float rel[2] = {static_cast<float>(pos[0] - kb - (kFp8 ? 0 : c4 * 2)),
+                                static_cast<float>(pos[1] - kb - (kFp8 ? 0 : c4 * 2))};
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float col = kFp8 ? static_cast<float>(nt * 8 + key_of_col(c4 * 2 + (k & 1)))
+                                     : static_cast<float>(nt * 8 + (k & 1));
+              s[nt][k] = fmaf(-map[k >> 1].slope2, fabsf(rel[k >> 1] - col),
+                              capped ? s[nt][k] : s[nt][k] * map[k >> 1].k);
+            }
+        }
+        if (partial) {
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int col = c4 * 2 + (k & 1);
+              const int key = kb + nt * 8 + (kFp8 ? key_of_col(col) : col);
+              if (key < span[k >> 1].lo || key > span[k >> 1].hi) s[nt][k] = -CUDART_INF_F;
+            }
         }
         float corr[2];
 #pragma unroll
@@ -555,7 +579,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2)) * mul[h];
           corr[h] = 1.f;
           if (mx > m[h] + kRescaleLog2) {
             corr[h] = ex2_approx(m[h] - mx);  // 0 for the first keys
@@ -576,8 +600,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float ref = m[h] == -CUDART_INF_F ? 0.f : m[h];
-            const float p0 = ex2_approx(s[nt][2 * h] - ref), p1 = ex2_approx(s[nt][2 * h + 1] - ref);
+            const float ref = m[h] == -CUDART_INF_F ? 0.f : -m[h];
+            const float p0 = ex2_approx(fmaf(s[nt][2 * h], mul[h], ref));
+            const float p1 = ex2_approx(fmaf(s[nt][2 * h + 1], mul[h], ref));
             l[h] += p0 + p1;
             pf[nt >> 1][h + 2 * (nt & 1)] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
@@ -623,16 +648,16 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
+              uint32_t f[4][2];  // f16x2 of codes 4 i, + 1 and 4 i + 2, + 3 of the four keys
+#pragma unroll
+              for (int k = 0; k < 4; ++k) f16x2_of_e4m3(u[k][i], f[k][0], f[k][1]);
 #pragma unroll
               for (int hw = 0; hw < 2; ++hw) {
-                uint32_t f[4];  // f16x2 of codes 4 i + 2 hw, + 1 of the four keys
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = f16x2_of_e4m3(u[k][i] >> (16 * hw));
                 const int nt = 4 * i + 2 * hw;
-                mma16816<true>(acc[nt], pf[ks], __byte_perm(f[0], f[1], 0x5410),
-                               __byte_perm(f[2], f[3], 0x5410));
-                mma16816<true>(acc[nt + 1], pf[ks], __byte_perm(f[0], f[1], 0x7632),
-                               __byte_perm(f[2], f[3], 0x7632));
+                mma16816<true>(acc[nt], pf[ks], __byte_perm(f[0][hw], f[1][hw], 0x5410),
+                               __byte_perm(f[2][hw], f[3][hw], 0x5410));
+                mma16816<true>(acc[nt + 1], pf[ks], __byte_perm(f[0][hw], f[1][hw], 0x7632),
+                               __byte_perm(f[2][hw], f[3][hw], 0x7632));
               }
             }
           }
@@ -976,34 +1001,54 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
     const int g = p.num_groups > 0 ? group_of[s] : -1;
     pc[0] = pieces_of(shared, g, kvh, tok, hg, p.group);
     pc[1] = pieces_of(own, s, kvh, tok, hg, p.group);
+    // 32 partials at a time: a lane reads the statistics of one each, the weights follow from their
+    // maximum, and then the loads of O depend on nothing but their index
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Line& ln = k == 0 ? shared : own;
-#pragma unroll 4
-      for (int i = sub; i < pc[k].count; i += kWpr) {
-        const int64_t at =
-            (pc[k].first + (pc[k].per == 2 ? i >> 1 : i)) * ln.rps + pc[k].in + (pc[k].per == 2 ? (i & 1) * 128 : 0);
-        const float2 ml = ln.part_ml[at];
-        float x[kVd];
-        if (kVd == 4) {
-          const float4 u = reinterpret_cast<const float4*>(ln.part_o + at * D)[lane];
-          x[0] = u.x;
-          x[1] = u.y;
-          x[kVd - 2] = u.z;
-          x[kVd - 1] = u.w;
-        } else {
-          const float2 u = reinterpret_cast<const float2*>(ln.part_o + at * D)[lane];
-          x[0] = u.x;
-          x[1] = u.y;
+      for (int i0 = sub; i0 < pc[k].count; i0 += 32 * kWpr) {
+        const int mine = i0 + lane * kWpr;
+        int64_t at = 0;
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (mine < pc[k].count) {
+          at = pc[k].per == 2 ? (pc[k].first + (mine >> 1)) * ln.rps + pc[k].in + (mine & 1) * 128
+                              : (pc[k].first + mine) * ln.rps + pc[k].in;
+          ml = ln.part_ml[at];
         }
-        const float mn = fmaxf(m, ml.x);
-        if (mn == -CUDART_INF_F) continue;  // no key seen so far
-        const float a = ex2_approx(m - mn), b = ex2_approx(ml.x - mn);
-        l = l * a + ml.y * b;
-        // a partial that saw no key may hold anything in O
+        float mn = ml.x;
 #pragma unroll
-        for (int c = 0; c < kVd; ++c) acc[c] = acc[c] * a + (b == 0.f ? 0.f : x[c] * b);
+        for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+        mn = fmaxf(mn, m);
+        if (mn == -CUDART_INF_F) continue;  // no key seen so far
+        const float w = ex2_approx(ml.x - mn), a = ex2_approx(m - mn);
+        float sum = w * ml.y;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l = l * a + sum;
         m = mn;
+#pragma unroll
+        for (int c = 0; c < kVd; ++c) acc[c] *= a;
+        const int cnt = min(32, (pc[k].count - i0 + kWpr - 1) / kWpr);
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          const float* src = ln.part_o + __shfl_sync(0xffffffffu, at, i) * D + lane * kVd;
+          float x[kVd];
+          if (kVd == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(src);
+            x[0] = u.x;
+            x[1] = u.y;
+            x[kVd - 2] = u.z;
+            x[kVd - 1] = u.w;
+          } else {
+            const float2 u = *reinterpret_cast<const float2*>(src);
+            x[0] = u.x;
+            x[1] = u.y;
+          }
+          // a partial that saw no key may hold anything in O
+#pragma unroll
+          for (int c = 0; c < kVd; ++c) acc[c] += wi == 0.f ? 0.f : x[c] * wi;
+        }
       }
     }
   }
