@@ -59,12 +59,12 @@ struct Piece {
   int ntiles;      // row tiles of the pair
   int tok;         // first query token of the pair
 };
-__device__ __forceinline__ Piece piece_at(const Cursor& c, int left, int tpt) {
+__device__ __forceinline__ Piece piece_of(const Walk& c, int tpt) {
   Piece p;
   p.kvh = c.j / c.w.nrt;
   p.pair = c.j - p.kvh * c.w.nrt;
-  p.t0 = c.t;
-  p.cnt = min(left, c.n - c.t);
+  p.t0 = c.t0;
+  p.cnt = c.cnt;
   p.ntiles = c.w.ntok - p.pair * 2 * tpt > tpt ? 2 : 1;
   p.tok = c.w.tok0 + p.pair * 2 * tpt;
   return p;
@@ -122,9 +122,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Cursor cur;
-  cur.seek(line, x0);
-  int left = x1 - x0;
+  Walk cur;
+  cur.enter(line, x0, x1);
 
   if (warp >= 8) {
     setmaxnreg_dec<kOtherRegs>();
@@ -134,8 +133,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int pieces = kTileKeys / rows;      // boxes of a tile along the keys
       int n = 0, k = 0;                         // ring entries, pieces of the line
       bool ok = true;
-      while (left > 0) {
-        const Piece w = piece_at(cur, left, line.tpt);
+      while (cur.next(p.hkv)) {
+        const Piece w = piece_of(cur, line.tpt);
         if (k > 0 && !__all_sync(kFull, mbar_wait(bar(kBarQEmpty), (k - 1) & 1, abort_flag))) {
           ok = false;
           break;
@@ -190,8 +189,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ++n;
         }
         if (!ok) break;
-        left -= w.cnt;
-        if (left > 0) cur.advance(w.cnt, p.hkv);
       }
       if (!ok) *abort_flag = 1;
       // every load in flight lands before shared memory is given up
@@ -228,8 +225,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ok = __all_sync(kFull, mbar_wait(bar(b), ph, abort_flag));
         return ok;
       };
-      while (left > 0) {
-        const Piece w = piece_at(cur, left, line.tpt);
+      while (cur.next(p.hkv)) {
+        const Piece w = piece_of(cur, line.tpt);
         if (!wait(kBarQ, k & 1)) break;
         ++k;
         bool o1 = false;
@@ -335,8 +332,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
           __syncwarp();
         }
-        left -= w.cnt;
-        if (left > 0) cur.advance(w.cnt, p.hkv);
       }
       if (!ok) *abort_flag = 1;
       if (elect_one()) mma_commit(bar(kBarDrain));
@@ -354,8 +349,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint32_t s_phase = 0, od_phase = 0;
     bool ok = true;
     int it = 0;
-    while (left > 0) {
-      const Piece w = piece_at(cur, left, line.tpt);
+    while (cur.next(p.hkv)) {
+      const Piece w = piece_of(cur, line.tpt);
       const int rt = w.ntiles == 2 ? t : 0;  // row tile that this warpgroup works on
       const int tk = w.tok + rt * line.tpt + row / p.group;
       const bool valid = row < line.tpt * p.group && tk < cur.w.tok0 + cur.w.ntok;
@@ -453,8 +448,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // warp's first P of that piece
         tc_fence_before();
       }
-      left -= w.cnt;
-      if (left > 0) cur.advance(w.cnt, p.hkv);
     }
     if (!ok) {
       *abort_flag = 1;
