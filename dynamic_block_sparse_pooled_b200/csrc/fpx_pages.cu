@@ -12,9 +12,18 @@ namespace fpx {
 namespace pages {
 
 constexpr int kThreads = 1024;
-// tokens up to which the planning CTA writes the slot map itself; above, a second launch does
-// (a launch costs about as much as one CTA takes for this many tokens)
+// Tokens up to which the planning CTA moves the pages and writes the slot map itself; above, a second
+// launch does both with the whole GPU (a launch costs about as much as one CTA takes for this many
+// tokens).
 constexpr int kInlineTokens = 4096;
+
+// What the planning CTA leaves for the second launch: pages given and taken before each request, and
+// in [num_seqs] their totals.
+struct Plan {
+  int32_t* give;
+  int32_t* take;
+  int32_t* ok;  // 1 where the call goes through
+};
 
 struct ResizeArgs {
   int num_seqs, page, log2_page, num_pages, pages_per_seq, token_capacity;
@@ -55,31 +64,26 @@ __device__ __forceinline__ bool change_of(const ResizeArgs& a, int s, Change& c)
   return true;
 }
 
-// Cache row of the token at position `pos` of request s: from its block table, or -1.
-__device__ __forceinline__ int slot_of(const ResizeArgs& a, int s, int pos, StatusBlock* st) {
-  const int pg = a.table[static_cast<int64_t>(s) * a.pages_per_seq + (pos >> a.log2_page)];
+// The last request s in [0, n) with off[s] <= i (off non-decreasing, off[0] = 0, i < off[n]): the one
+// that item i belongs to.
+__device__ __forceinline__ int owner_of(const int32_t* off, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = lo + ((hi - lo + 1) >> 1);
+    if (off[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Cache row of the token at position `pos` of request s, whose page is `pg`; -1 for a bad page.
+__device__ __forceinline__ int slot_at(const ResizeArgs& a, int pg, int s, int pos,
+                                       StatusBlock* st) {
   if (pg < 0 || pg >= a.num_pages) {
     record_error(st, FPX_ERR_DEVICE_INPUT, 51, s, pg);
     return -1;
   }
   return (pg << a.log2_page) + (pos & (a.page - 1));
-}
-
-__device__ __forceinline__ void write_token(const ResizeArgs& a, int t, int total,
-                                            StatusBlock* st) {
-  int slot = -1, pos = -1;
-  if (t < total) {
-    int lo = 0, hi = a.num_seqs - 1;  // largest s with cu_new[s] <= t
-    while (lo < hi) {
-      const int mid = lo + ((hi - lo + 1) >> 1);
-      if (a.cu_new[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    pos = a.lens[lo] + t - a.cu_new[lo];
-    slot = slot_of(a, lo, pos, st);
-  }
-  a.slots[t] = slot;
-  a.positions[t] = pos;
 }
 
 struct Sums {
@@ -95,12 +99,12 @@ __device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
 
 // One CTA: thread t owns a run of consecutive requests.  Pass 1 sums what they give, take and add;
 // a scan over the threads gives each its first place on the stack and among the tokens; the
-// totals are checked before anything is written.  Pass 2 writes cu_new and pushes the pages given
-// back; pass 3, after all pushes, pops.  The requests' lengths are read again in each pass.
+// totals are checked before anything is written.  Then, for few tokens, cu_new and the pushes, the
+// pops after all pushes, and the slot map; else cu_new and the plan of the second launch.
 // (The stack needs the requests' order, so the scan is the operator; it is latency-bound: two
-// reads of the lengths, the scan, one page write per page moved.)
-__global__ void __launch_bounds__(kThreads) resize_kernel(ResizeArgs a, int inline_tokens,
-                                                          StatusBlock* st) {
+// reads of the lengths and the scan.)
+template <bool kInline>
+__global__ void __launch_bounds__(kThreads) resize_kernel(ResizeArgs a, Plan plan, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
   __shared__ Sums warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -146,117 +150,235 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(ResizeArgs a, int inli
     if (tid == 0) {
       if (good) record_error(st, FPX_ERR_CAPACITY, 52, count, static_cast<int>(all.take));
       *a.free_count_out = count;
+      if (!kInline) *plan.ok = 0;
     }
     for (int s = tid; s <= a.num_seqs; s += kThreads) a.cu_new[s] = 0;
-    if (inline_tokens)
+    if (kInline)
       for (int t = tid; t < a.token_capacity; t += kThreads) a.slots[t] = a.positions[t] = -1;
     return;
   }
   const int top = count + static_cast<int>(all.give);
-  int give = count + static_cast<int>(at.give), tok = static_cast<int>(at.tokens);
+  const int total = static_cast<int>(all.tokens);
+  int give = static_cast<int>(at.give), take = static_cast<int>(at.take);
+  int tok = static_cast<int>(at.tokens);
   for (int s = s0; s < s1; ++s) {
     change_of(a, s, c);
     a.cu_new[s] = tok;
     tok += c.tokens;
-    const int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.first_give;
-    for (int i = 0; i < c.give; ++i) a.free_pages[give++] = row[i];
+    if (kInline) {
+      const int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.first_give;
+      for (int i = 0; i < c.give; ++i) a.free_pages[count + give++] = row[i];
+    } else {
+      plan.give[s] = give;
+      plan.take[s] = take;
+      give += c.give;
+      take += c.take;
+    }
   }
-  const int total = static_cast<int>(all.tokens);
   if (tid == 0) {
     a.cu_new[a.num_seqs] = total;
-    *a.free_count_out = top - static_cast<int>(all.take);
+    // a second launch reads the height as it was: it writes the new one (see moves_kernel)
+    if (kInline) *a.free_count_out = top - static_cast<int>(all.take);
+    if (!kInline) {
+      plan.give[a.num_seqs] = static_cast<int>(all.give);
+      plan.take[a.num_seqs] = static_cast<int>(all.take);
+      plan.ok[0] = 1;
+      plan.ok[1] = count;
+    }
   }
+  if (!kInline) return;
   __syncthreads();  // every push is on the stack, cu_new is written
-  int take = top - 1 - static_cast<int>(at.take);
   for (int s = s0; s < s1; ++s) {
     change_of(a, s, c);
     int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.have;
     for (int i = 0; i < c.take; ++i) {
-      const int pg = a.free_pages[take--];
+      const int pg = a.free_pages[top - 1 - take++];
       if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
       row[i] = pg;
     }
   }
-  if (!inline_tokens) return;
   __syncthreads();  // the table is written
-  for (int t = tid; t < a.token_capacity; t += kThreads) write_token(a, t, total, st);
+  for (int t = tid; t < a.token_capacity; t += kThreads) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int s = owner_of(a.cu_new, a.num_seqs, t);
+      pos = a.lens[s] + t - a.cu_new[s];
+      slot = slot_at(a, a.table[static_cast<int64_t>(s) * a.pages_per_seq + (pos >> a.log2_page)],
+                     s, pos, st);
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
 }
 
-// The slot map of many tokens: a thread each (8 bytes written, the rest from cache).
-__global__ void __launch_bounds__(256) slots_kernel(ResizeArgs a, StatusBlock* st) {
+// The page at place x of the stack after the pushes.  A page pushed by this call is looked up where
+// it comes from, so that no thread waits for another one's push.
+__device__ __forceinline__ int stack_at(const ResizeArgs& a, const Plan& plan, int count, int x) {
+  if (x < count) return a.free_pages[x];
+  const int i = x - count, s = owner_of(plan.give, a.num_seqs, i);
+  Change c;
+  change_of(a, s, c);
+  return a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.first_give + i - plan.give[s]];
+}
+
+// Pushes, pops and the slot map, a thread each (a request gives or takes, so no row of the table is
+// both read here and written; pushes go above the height that pops read below).
+__global__ void __launch_bounds__(256) moves_kernel(ResizeArgs a, Plan plan, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
-  const int t = blockIdx.x * blockDim.x + threadIdx.x;
-  if (t < a.token_capacity) write_token(a, t, a.cu_new[a.num_seqs], st);
+  const int first = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+  const bool ok = plan.ok[0] != 0;
+  const int count = plan.ok[1];
+  const int gives = ok ? plan.give[a.num_seqs] : 0, takes = ok ? plan.take[a.num_seqs] : 0;
+  const int total = a.cu_new[a.num_seqs];  // 0 where the call is refused
+  const int top = count + gives;
+  Change c;
+  if (ok && first == 0) *a.free_count_out = top - takes;
+  for (int i = first; i < gives; i += step) {
+    const int s = owner_of(plan.give, a.num_seqs, i);
+    change_of(a, s, c);
+    a.free_pages[count + i] =
+        a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.first_give + i - plan.give[s]];
+  }
+  for (int i = first; i < takes; i += step) {
+    const int s = owner_of(plan.take, a.num_seqs, i);
+    change_of(a, s, c);
+    const int pg = stack_at(a, plan, count, top - 1 - i);
+    if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
+    a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.have + i - plan.take[s]] = pg;
+  }
+  for (int t = first; t < a.token_capacity; t += step) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int s = owner_of(a.cu_new, a.num_seqs, t);
+      change_of(a, s, c);
+      pos = a.lens[s] + t - a.cu_new[s];
+      const int j = pos >> a.log2_page;
+      const int pg = j < c.have ? a.table[static_cast<int64_t>(s) * a.pages_per_seq + j]
+                                : stack_at(a, plan, count, top - 1 - (plan.take[s] + j - c.have));
+      slot = slot_at(a, pg, s, pos, st);
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
 }
 
 // ---- append -------------------------------------------------------------------------------------
 
-// x / scale as e4m3, round to nearest even, saturating (NaN stays NaN); the division is IEEE, so
-// the codes are those of the formula.
-__device__ __forceinline__ uint32_t quant2(float x, float y, float scale) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x, scale), __fdiv_rn(y, scale)),
-                                  __NV_SATFINITE, __NV_E4M3);
+// x / scale rounded to fp32 as by IEEE division, where that matters for an e4m3 code: the quotient by
+// the reciprocal, corrected once by its remainder (Markstein's step: exact to the last bit when the
+// reciprocal is correctly rounded).  Beyond 1024 the code saturates whatever the last bits are, and
+// the remainder could overflow.  Scales near the ends of fp32's range, whose reciprocal is not a
+// normal number, are divided by.  (3 multiply-adds instead of a division: 16384 rows 33 -> see the
+// measurement at append_kernel.)
+struct Divisor {
+  float s, r;
+  bool plain;
+  __device__ __forceinline__ void set(float scale) {
+    s = scale;
+    r = __fdiv_rn(1.f, scale);
+    plain = !(scale > 1e-30f && scale < 1e30f);
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    if (plain) return __fdiv_rn(x, s);
+    const float q = x * r;
+    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, x), r, q) : q;
+  }
+};
+// Two values as e4m3, round to nearest even, saturating (NaN stays NaN).
+__device__ __forceinline__ uint32_t quant2(float x, float y, const Divisor& d) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(d(x), d(y)), __NV_SATFINITE, __NV_E4M3);
 }
 
-// A thread moves 16 bytes of source of one K or V row (blockIdx.y) at a time: rows are [hkv, d], so
-// the copy is contiguous on both sides and bound by HBM; the slot is one cached read per row.
+constexpr int kBatch = 4;  // rows of a thread in flight
+
+// A thread keeps one 16-byte chunk c of the row [hkv, d] (so its head's scale too) and walks over the
+// tokens, kBatch at a time; neighbouring threads have neighbouring chunks, so both sides are
+// contiguous per row.  blockIdx.y: K or V.  Bound by HBM.
 template <bool kQuant>
 __global__ void __launch_bounds__(256) append_kernel(
-    int64_t chunks, int row_chunks, int chunks_per_head, const char* __restrict__ k,
-    int64_t k_stride, const char* __restrict__ v, int64_t v_stride,
-    const int32_t* __restrict__ slots, char* __restrict__ k_cache, char* __restrict__ v_cache,
-    int num_slots, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-    StatusBlock* st) {
+    int tokens, int row_chunks, int chunks_per_head, const char* __restrict__ k, int64_t k_stride,
+    const char* __restrict__ v, int64_t v_stride, const int32_t* __restrict__ slots,
+    char* __restrict__ k_cache, char* __restrict__ v_cache, int num_slots,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
   const bool is_v = blockIdx.y != 0;
   const char* src = is_v ? v : k;
   const int64_t stride = is_v ? v_stride : k_stride;
   char* dst = is_v ? v_cache : k_cache;
   const float* scale = is_v ? v_scale : k_scale;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < chunks;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int t = static_cast<int>(i / row_chunks), c = static_cast<int>(i - static_cast<int64_t>(t) * row_chunks);
-    const int slot = slots[t];
-    if (slot < 0) continue;
-    if (slot >= num_slots) {
-      if (c == 0) record_error(st, FPX_ERR_DEVICE_INPUT, 54, t, slot);
-      continue;
-    }
-    const uint4 x = *reinterpret_cast<const uint4*>(src + t * stride + c * 16);
-    if (kQuant) {
-      const float sc = scale[c / chunks_per_head];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-      uint32_t q[4];
+  const int span = min(row_chunks, 256), rows = 256 / span;  // chunks and tokens of a block
+  const int sub = threadIdx.x / span;
+  if (sub >= rows) return;
+  const int step = gridDim.x * rows;
+  for (int c = threadIdx.x - sub * span; c < row_chunks; c += span) {
+    Divisor div = {};
+    if (kQuant) div.set(scale[c / chunks_per_head]);
+    for (int64_t t0 = blockIdx.x * rows + sub; t0 < tokens; t0 += kBatch * static_cast<int64_t>(step)) {
+      int slot[kBatch];
+      uint4 x[kBatch];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[j] = quant2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u), sc);
-      *reinterpret_cast<uint2*>(dst + (static_cast<int64_t>(slot) * row_chunks + c) * 8) =
-          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-    } else {
-      *reinterpret_cast<uint4*>(dst + (static_cast<int64_t>(slot) * row_chunks + c) * 16) = x;
+      for (int b = 0; b < kBatch; ++b) {
+        const int64_t t = t0 + b * static_cast<int64_t>(step);
+        slot[b] = -1;
+        if (t < tokens) {
+          slot[b] = slots[t];
+          x[b] = __ldcs(reinterpret_cast<const uint4*>(src + t * stride + c * 16));
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (slot[b] < 0) continue;
+        if (slot[b] >= num_slots) {
+          if (c == 0)
+            record_error(st, FPX_ERR_DEVICE_INPUT, 54, static_cast<int>(t0) + b * step, slot[b]);
+          continue;
+        }
+        const int64_t at = static_cast<int64_t>(slot[b]) * row_chunks + c;
+        if (kQuant) {
+          const uint32_t u[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+          uint32_t q[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[j] = quant2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u), div);
+          *reinterpret_cast<uint2*>(dst + at * 8) =
+              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        } else {
+          *reinterpret_cast<uint4*>(dst + at * 16) = x[b];
+        }
+      }
     }
   }
 }
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-cudaError_t launch_resize(const ResizeArgs& a, StatusBlock* st, cudaStream_t s) {
-  const bool inline_tokens = a.token_capacity <= kInlineTokens;
-  FPX_CHAIN(resize_kernel, 1, kThreads, 0, s, a, inline_tokens ? 1 : 0, st);
-  if (!inline_tokens)
-    FPX_CHAIN(slots_kernel, static_cast<unsigned>((a.token_capacity - 1) / 256 + 1), 256, 0, s, a,
-              st);
+Plan plan_at(void* ws, int num_seqs) {
+  int32_t* base = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kStatusBytes);
+  return {base + 64, base + 64 + num_seqs + 1, base};
+}
+
+cudaError_t launch_resize(const ResizeArgs& a, void* ws, cudaStream_t s) {
+  StatusBlock* st = static_cast<StatusBlock*>(ws);
+  const Plan plan = plan_at(ws, a.num_seqs);
+  if (a.token_capacity <= kInlineTokens) {
+    FPX_CHAIN((resize_kernel<true>), 1, kThreads, 0, s, a, plan, st);
+    return cudaGetLastError();
+  }
+  FPX_CHAIN((resize_kernel<false>), 1, kThreads, 0, s, a, plan, st);
+  const int want = (a.token_capacity - 1) / 256 + 1;
+  FPX_CHAIN(moves_kernel, want < 148 * 8 ? want : 148 * 8, 256, 0, s, a, plan, st);
   return cudaGetLastError();
 }
 
 template <bool kQuant>
-cudaError_t launch_append(int64_t chunks, int row_chunks, int chunks_per_head, const void* k,
+cudaError_t launch_append(int tokens, int row_chunks, int chunks_per_head, const void* k,
                           int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots,
                           void* kc, void* vc, int num_slots, const float* ks, const float* vs,
                           StatusBlock* st, cudaStream_t s) {
-  const int64_t want = (chunks + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(want < 148 * 16 ? want : 148 * 16);
-  FPX_CHAIN((append_kernel<kQuant>), dim3(grid, 2), 256, 0, s, chunks, row_chunks, chunks_per_head,
+  const int rows = 256 / (row_chunks < 256 ? row_chunks : 256);
+  const int want = (tokens - 1) / rows + 1;
+  const unsigned grid = static_cast<unsigned>(want < 148 * 4 ? want : 148 * 4);
+  FPX_CHAIN((append_kernel<kQuant>), dim3(grid, 2), 256, 0, s, tokens, row_chunks, chunks_per_head,
             static_cast<const char*>(k), k_stride, static_cast<const char*>(v), v_stride, slots,
             static_cast<char*>(kc), static_cast<char*>(vc), num_slots, ks, vs, st);
   return cudaGetLastError();
@@ -270,7 +392,10 @@ using fpx::pages::is_aligned;
 
 extern "C" {
 
-size_t fpx_page_workspace_bytes(int32_t num_seqs) { return num_seqs < 1 ? 0 : kStatusBytes; }
+size_t fpx_page_workspace_bytes(int32_t num_seqs) {
+  if (num_seqs < 1) return 0;
+  return kStatusBytes + 256 + align_up(sizeof(int32_t) * 2 * (static_cast<size_t>(num_seqs) + 1), 256);
+}
 
 fpx_status fpx_page_resize(int32_t num_seqs, int32_t page, int32_t num_pages,
                            const int32_t* lens_d, const int32_t* new_lens_d,
@@ -315,8 +440,7 @@ fpx_status fpx_page_resize(int32_t num_seqs, int32_t page, int32_t num_pages,
   a.cu_new = cu_new_d;
   a.slots = slots_d;
   a.positions = positions_d;
-  return pages::launch_resize(a, static_cast<StatusBlock*>(ws),
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return pages::launch_resize(a, ws, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FPX_OK
              : FPX_ERR_CUDA;
 }
@@ -348,14 +472,13 @@ fpx_status fpx_kv_append(fpx_dtype dtype, int32_t hkv, int32_t d, int32_t num_to
   if (ws_bytes < kStatusBytes) return FPX_ERR_CAPACITY;
   if (num_tokens == 0) return FPX_OK;
   const int row_chunks = static_cast<int>(row * es / 16), per_head = static_cast<int>(d * es / 16);
-  const int64_t chunks = static_cast<int64_t>(num_tokens) * row_chunks;
   StatusBlock* st = static_cast<StatusBlock*>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      quant ? pages::launch_append<true>(chunks, row_chunks, per_head, k, k_stride * es, v,
+      quant ? pages::launch_append<true>(num_tokens, row_chunks, per_head, k, k_stride * es, v,
                                          v_stride * es, slots_d, k_cache, v_cache, num_slots,
                                          k_scale_d, v_scale_d, st, s)
-            : pages::launch_append<false>(chunks, row_chunks, per_head, k, k_stride * es, v,
+            : pages::launch_append<false>(num_tokens, row_chunks, per_head, k, k_stride * es, v,
                                           v_stride * es, slots_d, k_cache, v_cache, num_slots,
                                           nullptr, nullptr, st, s);
   return e == cudaSuccess ? FPX_OK : FPX_ERR_CUDA;
