@@ -625,7 +625,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // columns [c_lo, c_hi] of the block are seen by this row; no lane tests them where every
         // row of the warp sees the whole block
         const int c_lo = kRule ? span.lo - J * kTileN : 0, c_hi = kRule ? span.hi - J * kTileN : 0;
-        const bool partial = kRule && __any_sync(kFull, c_lo > 0 || c_hi < kTileN - 1);
+        const int partial = kRule ? (__any_sync(kFull, c_lo > 0) ? 1 : 0) |
+                                        (__any_sync(kFull, c_hi < kTileN - 1) ? 2 : 0)
+                                  : 0;
         const float rel = static_cast<float>(qpos - J * kTileN);
         // token causal mask (key column > query row) and token mask of one 64-column half
         auto mask_half = [&](uint32_t* x, int j0) {
@@ -676,7 +678,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
           }
         };
-        if (kCap && !kBias && !partial && map.k > 0.f) {
+        if (kCap && !kBias && partial == 0 && map.k > 0.f) {
           // a block that every row of the warp sees whole, all its scores well within the cap: the
           // maximum of the capped scores is that of the scores, so tanh and the exponential take
           // one pass over the row

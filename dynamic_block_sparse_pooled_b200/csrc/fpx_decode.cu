@@ -344,7 +344,6 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   // warps refills one behind, so that its first warp rarely waits for the others
   constexpr int kLag = RW == 1 ? 0 : 2;
   constexpr int kSteps = D / 16;  // k-steps of Q K^T, and pairs of n-tiles of P V
-  pdl_enter();  // after the previous kernel on the stream
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + kRing;
@@ -353,15 +352,15 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = warp / RW, wr = warp % RW;
   const int g4 = lane >> 2, c4 = lane & 3;
-  if (tid == 0) {
-    abort_flag_s = 0;
-    for (int i = 0; i < kGroups * kSlots; ++i) {
-      sm100::mbar_init(bars + i * kBarPitch, 1);       // full
-      sm100::mbar_init(bars + i * kBarPitch + 8, RW);  // empty
-    }
+  if (tid == 0) abort_flag_s = 0;
+  if (tid < kGroups * kSlots) {
+    sm100::mbar_init(bars + tid * kBarPitch, 1);       // full
+    sm100::mbar_init(bars + tid * kBarPitch + 8, RW);  // empty
     sm100::fence_mbar_init();
   }
+  static_assert(kGroups * kSlots <= kThreads, "one thread per slot");
   __syncthreads();
+  pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
   const int worker = blockIdx.x * kGroups + grp;
   const int64_t total = line.owners[line.n].line;
   const int64_t nw = active_workers(line, total);
@@ -760,7 +759,6 @@ decode_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   constexpr int kHalfD = D / 2;          // dimensions of a lane's part of a dot product
   constexpr int kQPitch = kHalfD + 4;    // the two halves of a Q row fall into different banks
   constexpr int kVd = D / 32;            // dimensions of a lane's part of O
-  pdl_enter();  // after the previous kernel on the stream
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -768,12 +766,13 @@ decode_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    abort_flag_s = 0;
-    for (int i = 0; i < kWarpsF32 * kSlots; ++i) sm100::mbar_init(bars + i * kBarPitch, 1);
+  if (tid == 0) abort_flag_s = 0;
+  if (tid < kWarpsF32 * kSlots) {
+    sm100::mbar_init(bars + tid * kBarPitch, 1);
     sm100::fence_mbar_init();
   }
   __syncthreads();
+  pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
   // Q rows [kRowsF32][2][kQPitch] and weights [kTileF32][kRowsF32] of this warp
   float* sq = reinterpret_cast<float*>(gbase + kWarpsF32 * kRingBytes + 1024) +
               warp * (kRowsF32 * 2 * kQPitch + kTileF32 * kRowsF32);

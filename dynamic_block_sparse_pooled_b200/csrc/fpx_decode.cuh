@@ -102,6 +102,7 @@ struct Walk {
   __device__ __forceinline__ void enter(const Line& l, int x0, int x1) {
     line = &l;
     left = x1 - x0;
+    if (left == 0) return;
     int lo = 0, hi = l.n - 1;  // the last owner with line <= x0: it has units, as x0 < total
     while (lo < hi) {
       const int mid = lo + ((hi - lo + 1) >> 1);

@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ DecodeDesc p,
                  const __grid_constant__ Line line, StatusBlock* st) {
-  pdl_enter();  // after the previous kernel on the stream
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -90,13 +89,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kOffBar + 8 * kNumBars + 4);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  const int64_t total = line.owners[line.n].line;
-  const int64_t nw = active_workers(line, total);
-  const int worker = blockIdx.x;
-  if (worker >= nw) return;  // the whole CTA
-  const int x0 = static_cast<int>(line_begin(worker, total, nw));
-  const int x1 = static_cast<int>(line_begin(worker + 1, total, nw));
 
   if (tid == 0) {
     mbar_init(bar(kBarQ), 1);
@@ -122,6 +114,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
+  const int64_t total = line.owners[line.n].line;
+  const int64_t nw = active_workers(line, total);
+  const int worker = blockIdx.x;
+  // a CTA without work has an empty stretch: it goes through the roles' ends like the others
+  const int x0 = worker < nw ? static_cast<int>(line_begin(worker, total, nw)) : 0;
+  const int x1 = worker < nw ? static_cast<int>(line_begin(worker + 1, total, nw)) : 0;
   Walk cur;
   cur.enter(line, x0, x1);
 
@@ -368,7 +367,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (!((uses_of(w, e) >> t) & 1)) continue;
         const int kb = cur.w.k0 + (w.t0 + e) * kTileKeys;
         const int c_lo = rp.span.lo - kb, c_hi = rp.span.hi - kb;
-        const bool partial = __any_sync(kFull, c_lo > 0 || c_hi < kTileKeys - 1);
+        const int partial = (__any_sync(kFull, c_lo > 0) ? 1 : 0) |
+                            (__any_sync(kFull, c_hi < kTileKeys - 1) ? 2 : 0);
         const float rel = static_cast<float>(rp.i - kb);
         if (!__all_sync(kFull, mbar_wait(bar(kBarSFull + t), s_phase, abort_flag))) {
           ok = false;
