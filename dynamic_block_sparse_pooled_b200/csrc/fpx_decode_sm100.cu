@@ -40,7 +40,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr uint32_t kBox = 128 * 128;       // 128 rows x 128 bytes
 constexpr uint32_t kSlot = 2 * kBox;       // 128 x 128 bf16
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kSlot, kOffV = 4 * kSlot, kOffBar = 6 * kSlot;
-constexpr size_t kTcSmem = 6 * kSlot + 256 + 1024;
+constexpr size_t kTcSmem = 6 * kSlot + 512 + 1024;
 constexpr int kSteps = kDim / 16;
 constexpr uint32_t kIdescQK = make_idesc(1, 1, false, 128, 128);
 constexpr uint32_t kIdescPV = make_idesc(1, 1, true, 128, 128);
@@ -49,31 +49,35 @@ enum Bar {
   kBarQ = 0, kBarQEmpty = 1,
   kBarKFull = 2, kBarKEmpty = 4, kBarVFull = 6, kBarVEmpty = 8,  // + slot
   kBarSFull = 10, kBarPReady = 12, kBarODone = 14,               // + tile
-  kBarDrain = 16, kNumBars = 17
+  kBarDrain = 16,
+  kBarUFull = 17, kBarUEmpty = 19,                               // + slot of the piece ring
+  kNumBars = 21
 };
+constexpr int kReaders = 9;  // the MMA warp and the eight softmax warps
 
-// A stretch of key tiles of one segment.
+// A stretch of key tiles of one segment, as the load warp hands it to the other roles through a
+// two-slot ring in shared memory (they would each spend registers on the walk along the line).
 struct Piece {
-  int kvh, pair;   // KV head, pair of row tiles
-  int t0, cnt;     // key tiles
+  int cnt;         // key tiles; 0 ends the CTA's work
+  int key0, k1;    // first key, end of the segment's range
+  int kvh;
   int ntiles;      // row tiles of the pair
-  int tok;         // first query token of the pair
+  int tok, tok1;   // first query token of the pair, end of the group's
+  int slot;        // partial slot
 };
-__device__ __forceinline__ Piece piece_of(const Walk& c, int tpt) {
+__device__ __forceinline__ Piece piece_of(const Walk& c, int tpt, int worker) {
   Piece p;
   p.kvh = c.j / c.w.nrt;
-  p.pair = c.j - p.kvh * c.w.nrt;
-  p.t0 = c.t0;
+  const int pair = c.j - p.kvh * c.w.nrt;
   p.cnt = c.cnt;
-  p.ntiles = c.w.ntok - p.pair * 2 * tpt > tpt ? 2 : 1;
-  p.tok = c.w.tok0 + p.pair * 2 * tpt;
+  p.key0 = c.w.k0 + c.t0 * kTileKeys;
+  p.k1 = c.w.k1;
+  p.ntiles = c.w.ntok - pair * 2 * tpt > tpt ? 2 : 1;
+  p.tok = c.w.tok0 + pair * 2 * tpt;
+  p.tok1 = c.w.tok0 + c.w.ntok;
+  p.slot = c.w.seg + c.j + worker;
   return p;
 }
-// The row tiles (softmax warpgroups) that use key tile e of a piece, as bits.
-__device__ __forceinline__ int uses_of(const Piece& p, int e) {
-  return p.ntiles == 2 ? 3 : 1 << (e & 1);
-}
-
 template <bool kCap, bool kBias>
 __global__ void __launch_bounds__(kTcThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -87,6 +91,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t bar0 = sbase + kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kOffBar + 8 * kNumBars + 4);
+  Piece* ring = reinterpret_cast<Piece*>(gbase + kOffBar + 256);
+  static_assert(8 * kNumBars + 8 <= 256 && 2 * sizeof(Piece) <= 256, "shared memory layout");
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -102,6 +108,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(bar(kBarPReady + i), 4);  // one arrival per softmax warp
       mbar_init(bar(kBarODone + i), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarUFull + i), 1);
+      mbar_init(bar(kBarUEmpty + i), kReaders);
+    }
     mbar_init(bar(kBarDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -115,14 +125,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
-  const int64_t total = line.owners[line.n].line;
-  const int64_t nw = active_workers(line, total);
-  const int worker = blockIdx.x;
-  // a CTA without work has an empty stretch: it goes through the roles' ends like the others
-  const int x0 = worker < nw ? static_cast<int>(line_begin(worker, total, nw)) : 0;
-  const int x1 = worker < nw ? static_cast<int>(line_begin(worker + 1, total, nw)) : 0;
-  Walk cur;
-  cur.enter(line, x0, x1);
+  // Piece k of this CTA; false on a timeout.  Warp-uniform.
+  auto take_piece = [&](int k, Piece& w) -> bool {
+    if (!__all_sync(kFull, mbar_wait(bar(kBarUFull + (k & 1)), (k >> 1) & 1, abort_flag)))
+      return false;
+    w = ring[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarUEmpty + (k & 1)));
+    return true;
+  };
 
   if (warp >= 8) {
     setmaxnreg_dec<kOtherRegs>();
@@ -132,8 +143,30 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int pieces = kTileKeys / rows;      // boxes of a tile along the keys
       int n = 0, k = 0;                         // ring entries, pieces of the line
       bool ok = true;
-      while (cur.next(p.hkv)) {
-        const Piece w = piece_of(cur, line.tpt);
+      const int64_t total = line.owners[line.n].line;
+      const int64_t nw = active_workers(line, total);
+      const int worker = blockIdx.x;
+      Walk cur;
+      if (worker < nw)
+        cur.enter(line, static_cast<int>(line_begin(worker, total, nw)),
+                  static_cast<int>(line_begin(worker + 1, total, nw)));
+      else
+        cur.left = 0;
+      int u = 0;  // pieces published
+      while (true) {
+        Piece w = {};
+        if (cur.next(p.hkv)) w = piece_of(cur, line.tpt, worker);
+        if (!__all_sync(kFull, mbar_wait(bar(kBarUEmpty + (u & 1)), ((u >> 1) & 1) ^ 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          ring[u & 1] = w;
+          mbar_arrive(bar(kBarUFull + (u & 1)));  // release: the slot's write is visible first
+        }
+        __syncwarp();
+        ++u;
+        if (w.cnt == 0) break;
         if (k > 0 && !__all_sync(kFull, mbar_wait(bar(kBarQEmpty), (k - 1) & 1, abort_flag))) {
           ok = false;
           break;
@@ -153,8 +186,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const uint32_t ph = (n >> 1) & 1;
           // cache row of box `lane`; behind the range's end or outside the cache: zeros
           int row = p.num_pages << p.log2_page;
-          const int key = cur.w.k0 + (w.t0 + e) * kTileKeys + lane * rows;
-          if (lane < pieces && key < cur.w.k1) {
+          const int key = w.key0 + e * kTileKeys + lane * rows;
+          if (lane < pieces && key < w.k1) {
             const int pg = p.table[static_cast<int64_t>(cur.w.row) * p.pages_per_seq + (key >> p.log2_page)];
             if (pg < 0 || pg >= p.num_pages)
               record_error(st, FPX_ERR_DEVICE_INPUT, 70, cur.w.row, key >> p.log2_page);
@@ -224,8 +257,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ok = __all_sync(kFull, mbar_wait(bar(b), ph, abort_flag));
         return ok;
       };
-      while (cur.next(p.hkv)) {
-        const Piece w = piece_of(cur, line.tpt);
+      while (true) {
+        Piece w;
+        if (!take_piece(k, w)) {
+          ok = false;
+          break;
+        }
+        if (w.cnt == 0) break;
         if (!wait(kBarQ, k & 1)) break;
         ++k;
         bool o1 = false;
@@ -348,24 +386,30 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint32_t s_phase = 0, od_phase = 0;
     bool ok = true;
     int it = 0;
-    while (cur.next(p.hkv)) {
-      const Piece w = piece_of(cur, line.tpt);
+    for (int k = 0;; ++k) {
+      Piece w;
+      if (!take_piece(k, w)) {
+        ok = false;
+        break;
+      }
+      if (w.cnt == 0) break;
       const int rt = w.ntiles == 2 ? t : 0;  // row tile that this warpgroup works on
       const int tk = w.tok + rt * line.tpt + row / p.group;
-      const bool valid = row < line.tpt * p.group && tk < cur.w.tok0 + cur.w.ntok;
+      const bool valid = row < line.tpt * p.group && tk < w.tok1;
       const int head = w.kvh * p.group + row % p.group;
       RowPos rp = row_pos(p, valid ? tk : w.tok);
       if (!valid) rp.span = {0, INT_MAX};  // discarded: no reason to mask
-      rp.span.hi = min(rp.span.hi, cur.w.k1 - 1);
+      rp.span.hi = min(rp.span.hi, w.k1 - 1);
       const ScoreMap map = score_map(p.rule, p.scale, head);
       TanhPoly poly = {};
       if (kCap) poly.set(map.cap2);
       const float sl2 = kCap || kBias ? 1.f : map.k;
       float m_ref = -CUDART_INF_F, l_run = 0.f;
       it = 0;
-      for (int e = 0; e < w.cnt; ++e) {
-        if (!((uses_of(w, e) >> t) & 1)) continue;
-        const int kb = cur.w.k0 + (w.t0 + e) * kTileKeys;
+      // with one row tile the two warpgroups take the key tiles in turn
+      const int stride = w.ntiles == 2 ? 1 : 2;
+      for (int e = w.ntiles == 2 ? 0 : t; e < w.cnt; e += stride) {
+        const int kb = w.key0 + e * kTileKeys;
         const int c_lo = rp.span.lo - kb, c_hi = rp.span.hi - kb;
         const int partial = (__any_sync(kFull, c_lo > 0) ? 1 : 0) |
                             (__any_sync(kFull, c_hi < kTileKeys - 1) ? 2 : 0);
@@ -421,7 +465,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       if (!ok) break;
       // the piece's partial: tile t's rows are 128 t .. 128 t + 127 of the slot
-      const int64_t at = (static_cast<int64_t>(cur.w.seg) + cur.j + worker) * line.rps + t * 128 + row;
+      const int64_t at = static_cast<int64_t>(w.slot) * line.rps + t * 128 + row;
       if (valid) line.part_ml[at] = make_float2(m_ref, l_run);
       if (it > 0) {
         if (!__all_sync(kFull, mbar_wait(bar(kBarODone + t), od_phase, abort_flag))) {
@@ -451,7 +495,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     if (!ok) {
       *abort_flag = 1;
-      if (row == 0) record_error(st, FPX_ERR_TIMEOUT, 71, worker, it);
+      if (row == 0) record_error(st, FPX_ERR_TIMEOUT, 71, static_cast<int>(blockIdx.x), it);
     }
   }
   tc_fence_before();
