@@ -43,6 +43,8 @@ KERNELS_PER_STEP = 10  # plan+pool+score, plan+count+scan+emit, plan+order+atten
 # Reported as roofline.traffic only while the sources still have that digest; any change to the
 # kernel makes it null until it is measured again.
 ATTN_SOURCES = ("dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cu",
+                "dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cuh",
+                "dynamic_block_sparse_pooled_b200/csrc/fpx_softmax.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_sm100.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_common.cuh")
 ATTN_TRAFFIC_DIGEST = "f88c351c7ee3c84bab085496a3a55124c32d919be05b2a163c66a83baa3ea018"

@@ -543,7 +543,7 @@ def score_rule(softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, wind
 
 
 def _check_rule(rule: ScoreRule, hq: int, tokens: int, device: int) -> None:
-    slopes, lo, hi = rule._keep
+    slopes, lo, hi = getattr(rule, "_keep", (None, None, None))
     _expect("slopes", slopes, torch.float32, device, hq)
     _expect("key_lo", lo, torch.int32, device, tokens)
     _expect("key_hi", hi, torch.int32, device, tokens)
@@ -585,6 +585,7 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
                 nnz=None, capacity: Optional[int] = None, stream=None):
     """fpx_span_select -> (row_ptr, col_idx, nnz): the key blocks that the rule's spans reach."""
     dev, index = ws.device, ws.get_device()
+    _expect("ws", ws, torch.uint8, index)
     _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, index)
     if row_ptr is None:
         row_ptr = torch.empty(pf.rows + 1, dtype=torch.int32, device=dev)
@@ -624,6 +625,7 @@ def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         lse = torch.empty((p.hq, p.total_tokens), dtype=torch.float32, device=q.device)
     _expect("o", o, odt, dev, shape=q.shape)
     _expect("lse", lse, torch.float32, dev, p.hq * p.total_tokens)
+    _expect("ws", ws, torch.uint8, dev)
     _call("fpx_span_prefill", dev, stream, pf.ptr, _ptr(q), _ptr(k), _ptr(v),
           ctypes.byref(kv) if kv is not None else None, ctypes.byref(rule), _ptr(row_ptr),
           _ptr(col_idx), _ptr(o), _ptr(lse), _ptr(ws), ws.numel())
@@ -687,6 +689,7 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     _expect("cu_new", cu_new, i32, dev, n + 1)
     _expect("slots", slots, i32, dev, token_capacity)
     _expect("positions", positions, i32, dev, token_capacity)
+    _expect("ws", ws, torch.uint8, dev)
     _call("fpx_page_resize", dev, stream, n, page, num_pages, lens.data_ptr(),
           new_lens.data_ptr(), _ptr(keep_pages), block_table.data_ptr(), block_table.shape[1],
           free_pages.data_ptr(), free_count.data_ptr(), count_out.data_ptr(), cu_new.data_ptr(),
@@ -725,6 +728,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: to
     _expect("slots", slots, torch.int32, dev, n)
     _expect("k_scale", k_scale, torch.float32, dev, hkv)
     _expect("v_scale", v_scale, torch.float32, dev, hkv)
+    _expect("ws", ws, torch.uint8, dev)
     _call("fpx_kv_append", dev, stream, _DTYPES[k_cache.dtype], hkv, d, n, k.data_ptr(),
           strides[0], v.data_ptr(), strides[1], slots.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), rows, _ptr(k_scale), _ptr(v_scale), ws.data_ptr(), ws.numel())
@@ -813,6 +817,7 @@ def decode(dp: Decode, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         _expect("lse", lse, torch.float32, dev, p.hq * tokens)
     elif want_lse:
         lse = torch.empty((p.hq, tokens), dtype=torch.float32, device=dp.device)
+    _expect("ws", ws, torch.uint8, dev)
     _call("fpx_decode", dev, stream, dp.ptr, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           ctypes.byref(rule) if rule is not None else None, o.data_ptr(), _ptr(lse),
           ws.data_ptr(), ws.numel())

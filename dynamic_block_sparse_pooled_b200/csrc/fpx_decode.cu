@@ -1254,10 +1254,11 @@ size_t decode_workspace(const decode::DecodeDesc& p, fpx_dtype dt) {
 
 bool decode_fits(const decode::DecodeDesc& p, fpx_dtype dt) {
   const decode::Layout L = decode::layout_of(p, dt);
-  const double tiles = static_cast<double>(p.pages_per_seq) * p.page / 16 + 1 + decode::kPad + decode::kPadTc;
+  const double keys = static_cast<double>(p.pages_per_seq) * p.page;
   const double rows = static_cast<double>(p.q_len) * p.group;
-  const double own = tiles * p.num_seqs * p.hkv * (rows / L.own.rt + 1);
-  const double shared = tiles * p.hkv * (rows * p.num_seqs / L.shared.rt + p.num_groups + 1);
+  const double own = (keys / L.own.tile + 1 + L.own.pad) * p.num_seqs * p.hkv * (rows / L.own.rt + 1);
+  const double shared = (keys / L.shared.tile + 1 + L.shared.pad) * p.hkv *
+                        (rows * p.num_seqs / L.shared.rt + p.num_groups + 1);
   return own < INT32_MAX && shared < INT32_MAX;
 }
 

@@ -16,6 +16,10 @@
  *                      blocks only, token-causal inside the diagonal block; O and per-row LSE
  *                      (App. B, "Block Sparse Attention").
  *
+ * Next to them stand the operators of the serving step around a prefill: attention under a score
+ * rule (fpx_span_*), block tables and slot maps (fpx_page_resize), the cache write (fpx_kv_append) and
+ * decode over the paged cache with shared prompts (fpx_decode).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Layouts.  Q is [T, Hq, D], K and V are [T, Hkv, D], row-major and contiguous ("packed THD"),
@@ -388,15 +392,16 @@ fpx_status fpx_kv_append(fpx_dtype dtype, int32_t hkv, int32_t d, int32_t num_to
  * i = ctx_lens[s] - q_len + t and sees what the rule lets it see (rule NULL: keys 0 .. i); a
  * negative position sees no key, so an unused entry of a batch has ctx_lens 0.
  * Groups: the requests group_ptr[g] .. group_ptr[g + 1] - 1 share their first prefix_pages[g] pages
- * (a system prompt): that part is read from the block-table row of the group's FIRST request and is
- * loaded once for the whole group instead of once per request.  Requests of no group share
- * nothing.  Same result as without groups, up to rounding.
+ * (a system prompt); their block-table rows name the same pages there.  That part is read once for
+ * the whole group, from the row of its FIRST request (which may itself be an unused entry), instead
+ * of once per request.  Requests of no group share nothing.  Same result as without groups, up to
+ * rounding.
  *   q   device [num_seqs * q_len, hq, d], bf16 (FPX_BF16 and FPX_E4M3 caches) or fp32 (FPX_F32).
  *   k_cache, v_cache  device [num_pages, page, hkv, d] in `dtype`; FPX_E4M3 values are multiplied
- *       by k_scale / v_scale of their head.  Every row below ctx_lens must be finite unless no
- *       query of its request sees a key within 32 positions of it; rows at and beyond ctx_lens may
- *       hold anything.
+ *       k_scale / v_scale of their head.  Rows at and beyond ctx_lens may hold anything; rows below
+ *       it must be finite, as a key that is not seen counts with weight zero.
  *   o   device [num_seqs * q_len, hq, d] in q's type;  lse  device fp32 [hq, num_seqs * q_len] or NULL.
+ *   ws  device workspace >= fpx_decode_workspace_bytes(p); calls that may overlap need one each.
  *   ctx_lens_d beyond the block table (pages_per_seq * page), or negative: FPX_ERR_DEVICE_INPUT is
  *       recorded and it is clamped.  group_ptr that decreases or leaves [0, num_seqs], or
  *       negative prefix_pages: FPX_ERR_DEVICE_INPUT, O = 0 and LSE = -inf everywhere.  A page

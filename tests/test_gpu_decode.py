@@ -332,3 +332,33 @@ def test_queries_far_from_one(gain):
     big = gain > 1
     rule = fpx.score_rule(5.0) if big else None
     c.check(*c.run(rule), **({"softcap": 5.0} if big else {}))
+
+
+def test_two_calls_at_once():
+    """Two problems on two streams, each with its own workspace, give what they give alone."""
+    cases = [Case("bf16", [3000 + 13 * i for i in range(40)], 8, 2, 128, 128, groups=[0, 40],
+                  prefix=[20], seed=16),
+             Case("e4m3", [900 + 131 * i for i in range(20)], 6, 2, 128, 32, 3, seed=17)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, c in enumerate(cases):
+            got[i].append(fpx.decode(c.dp, c.qd, c.k, c.v, c.ws, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+        assert fpx.status(c.ws) == 0
+
+
+def test_rule_of_another_size_is_refused():
+    c = Case("bf16", [40, 50], 4, 2, 128, 32, seed=18)
+    short = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        c.run(fpx.score_rule(key_lo=short, key_hi=short))
+    with pytest.raises(ValueError):
+        c.run(fpx.score_rule(slopes=torch.zeros(3, device="cuda")))
+    with pytest.raises(ValueError):
+        c.run(fpx.score_rule(slopes=torch.zeros(4)))

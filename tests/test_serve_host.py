@@ -237,6 +237,8 @@ def test_page_and_append_wrappers():
         fpx.page_resize(i32(3), i32(3), i32(3, 4), i32(9), i32(1), 16, 9, 10, ws, slots=i32(9))
     with pytest.raises(TypeError):
         fpx.page_resize(i32(3).long(), i32(3), i32(3, 4), i32(9), i32(1), 16, 9, 10, ws)
+    with pytest.raises(TypeError):
+        fpx.page_resize(i32(3), i32(3), i32(3, 4), i32(9), i32(1), 16, 9, 10, i32(64))
     k = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     c = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)
     for args in ((k.float(), k, i32(4), c, c), (k, k[:3], i32(4), c, c), (k, k, i32(3), c, c),
