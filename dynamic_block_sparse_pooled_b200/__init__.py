@@ -497,7 +497,9 @@ def vs_path(q, k, v, block: int, n_probe: int, alpha_v: float, alpha_s: float, c
 def _expect(name: str, t: Optional[torch.Tensor], dtype, device: int = -2, numel: int = 0,
             shape=None) -> None:
     """Refuses a tensor that the device code would misread (None passes; device: its index)."""
-    if t is None:
+    if t is None or (t.dtype is dtype and (device == -2 or t.get_device() == device) and
+                     t.is_contiguous() and t.numel() >= numel and
+                     (shape is None or t.shape == shape)):
         return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -507,8 +509,7 @@ def _expect(name: str, t: Optional[torch.Tensor], dtype, device: int = -2, numel
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} entries, needs {numel}")
+    raise ValueError(f"{name} holds {t.numel()} entries, needs {numel}")
 
 
 def _call(name: str, device: int, stream, *args) -> None:
@@ -671,14 +672,13 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     count_out = free_count if count_out is None else count_out
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table must be [num_seqs, pages_per_seq]")
-    on = lens.device
-    if cu_new is None:
-        cu_new = torch.empty(n + 1, dtype=torch.int32, device=on)
-    if slots is None:
-        slots = torch.empty(token_capacity, dtype=torch.int32, device=on)
-    if positions is None:
-        positions = torch.empty(token_capacity, dtype=torch.int32, device=on)
     i32 = torch.int32
+    if cu_new is None:
+        cu_new = torch.empty(n + 1, dtype=i32, device=lens.device)
+    if slots is None:
+        slots = torch.empty(token_capacity, dtype=i32, device=lens.device)
+    if positions is None:
+        positions = torch.empty(token_capacity, dtype=i32, device=lens.device)
     _expect("lens", lens, i32, dev)
     _expect("new_lens", new_lens, i32, dev, n)
     _expect("keep_pages", keep_pages, i32, dev, n)

@@ -181,6 +181,50 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeDesc p, Line o
   if (p.num_groups > 0) scan_line(shared, p.hkv, warp_sum);
 }
 
+// Few requests and nothing shared: every CTA lays the line out for itself in shared memory instead of
+// waiting for a launch that does (one warp; 3 requests 19.5 -> see launch_decode).
+constexpr int kLocalSeqs = 64;
+
+__device__ __forceinline__ void plan_local(const DecodeDesc& p, Line& l, Owner* owners,
+                                           StatusBlock* st) {
+  l.owners = owners;
+  const int lane = threadIdx.x;
+  if (lane < 32) {
+    const int most = p.pages_per_seq << p.log2_page;
+    const int nrt = (p.q_len * p.group + l.rt - 1) / l.rt;
+    int line = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+      const int s = s0 + lane;
+      Owner w = {0, 0, s * p.q_len, p.q_len, s, 0, s * nrt * p.hkv, nrt};
+      if (s < p.num_seqs) {
+        int ctx = p.ctx[s];
+        if (ctx < 0 || ctx > most) {
+          record_error(st, FPX_ERR_DEVICE_INPUT, 61, s, ctx);
+          ctx = min(max(ctx, 0), most);
+        }
+        const int lo = p.rule.window > 0 ? max(ctx - p.q_len, 0) - min(p.rule.window - 1, most) : 0;
+        w.k0 = lo > 0 ? lo / 32 * 32 : 0;
+        w.k1 = max(ctx, w.k0);
+      }
+      const int mine = units_of(w, l) * nrt * p.hkv;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      w.line = line + x - mine;
+      if (s < p.num_seqs) owners[s] = w;
+      line += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      Owner end = {0, 0, 0, 0, 0, line, p.num_seqs * nrt * p.hkv, 0};
+      owners[p.num_seqs] = end;
+    }
+  }
+  __syncthreads();
+}
+
 // ---- the ring -----------------------------------------------------------------------------------
 
 // Layout of a half-stage: kTile keys x D elements as boxes of kRowB bytes per key.
@@ -334,7 +378,7 @@ constexpr int kTile = 32;  // keys
 template <bool kFp8, int D, int RW>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ DecodeDesc p, const __grid_constant__ Line line,
+                  const __grid_constant__ DecodeDesc p, const __grid_constant__ Line line_,
                   const __nv_bfloat16* __restrict__ q, StatusBlock* st) {
   using H = Half<kFp8 ? 1 : 2, D, kTile>;
   constexpr unsigned kFull = 0xffffffffu;
@@ -361,6 +405,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   static_assert(kGroups * kSlots <= kThreads, "one thread per slot");
   __syncthreads();
   pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
+  __shared__ Owner local[kLocalSeqs + 1];
+  Line line = line_;
+  if (!line.owners) plan_local(p, line, local, st);
   const int worker = blockIdx.x * kGroups + grp;
   const int64_t total = line.owners[line.n].line;
   const int64_t nw = active_workers(line, total);
@@ -751,7 +798,7 @@ constexpr int kWarpsF32 = 7;  // an eighth ring would not leave room for the Q r
 template <int D>
 __global__ void __launch_bounds__(kWarpsF32 * 32, 1)
 decode_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ DecodeDesc p, const __grid_constant__ Line line,
+                  const __grid_constant__ DecodeDesc p, const __grid_constant__ Line line_,
                   const float* __restrict__ q, StatusBlock* st) {
   using H = Half<4, D, kTileF32>;
   constexpr unsigned kFull = 0xffffffffu;
@@ -773,6 +820,9 @@ decode_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   __syncthreads();
   pdl_enter();  // after the previous kernel on the stream, which the set-up above overlaps
+  __shared__ Owner local[kLocalSeqs + 1];
+  Line line = line_;
+  if (!line.owners) plan_local(p, line, local, st);
   // Q rows [kRowsF32][2][kQPitch] and weights [kTileF32][kRowsF32] of this warp
   float* sq = reinterpret_cast<float*>(gbase + kWarpsF32 * kRingBytes + 1024) +
               warp * (kRowsF32 * 2 * kQPitch + kTileF32 * kRowsF32);
@@ -991,11 +1041,15 @@ __device__ __forceinline__ Pieces pieces_of(const Line& l, int owner, int kvh, i
 // Several warps per row shorten the chain of loads when there are few rows and many partials.
 template <typename OT, int D, int kWpr>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ DecodeDesc p,
-                                                   const __grid_constant__ Line own,
+                                                   const __grid_constant__ Line own_,
                                                    const __grid_constant__ Line shared,
                                                    const int32_t* __restrict__ group_of,
-                                                   OT* __restrict__ o, float* __restrict__ lse) {
+                                                   OT* __restrict__ o, float* __restrict__ lse,
+                                                   StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
+  __shared__ Owner local[kLocalSeqs + 1];
+  Line own = own_;
+  if (!own.owners) plan_local(p, own, local, st);
   constexpr int kVd = D / 32;
   __shared__ float sm[8], sl[8], so[8][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1179,13 +1233,11 @@ static bool make_cache_map(CUtensorMap* map, const void* base, int rows, int hkv
 template <bool kFp8, int D, int RW>
 static cudaError_t launch_mma_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeDesc& p,
                                 const Line& line, const void* q, StatusBlock* st, cudaStream_t s) {
-  auto kern = decode_mma_kernel<kFp8, D, RW>;
   constexpr size_t smem =
       1024 + kRing + kBarPitch * kWarps * Half<kFp8 ? 1 : 2, D, kTile>::kSlots1;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = allow_smem<decode_mma_kernel<kFp8, D, RW>>(smem);
   if (e != cudaSuccess) return e;
-  FPX_CHAIN(kern, kCtas, kThreads, smem, s, mk, mv, p, line,
+  FPX_CHAIN((decode_mma_kernel<kFp8, D, RW>), kCtas, kThreads, smem, s, mk, mv, p, line,
             static_cast<const __nv_bfloat16*>(q), st);
   return cudaGetLastError();
 }
@@ -1205,16 +1257,14 @@ static cudaError_t launch_mma(const CUtensorMap& mk, const CUtensorMap& mv, cons
 template <int D>
 static cudaError_t launch_f32(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeDesc& p,
                               const Line& line, const void* q, StatusBlock* st, cudaStream_t s) {
-  auto kern = decode_f32_kernel<D>;
   constexpr size_t smem =
       1024 + kWarpsF32 * kRingBytes + 1024 +
       kWarpsF32 * sizeof(float) * (kRowsF32 * 2 * (D / 2 + 4) + kTileF32 * kRowsF32);
   static_assert(kBarPitch * kWarpsF32 * Half<4, D, kTileF32>::kSlots1 <= 1024, "barriers");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = allow_smem<decode_f32_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
-  FPX_CHAIN(kern, kCtas, kWarpsF32 * 32, smem, s, mk, mv, p, line, static_cast<const float*>(q),
-            st);
+  FPX_CHAIN(decode_f32_kernel<D>, kCtas, kWarpsF32 * 32, smem, s, mk, mv, p, line,
+            static_cast<const float*>(q), st);
   return cudaGetLastError();
 }
 
@@ -1233,16 +1283,16 @@ static cudaError_t launch_line(const CUtensorMap& mk, const CUtensorMap& mv, con
 
 template <typename OT, int D>
 static cudaError_t launch_join(const DecodeDesc& p, const Line& own, const Line& shared,
-                               const int32_t* group_of, void* o, float* lse, cudaStream_t s) {
+                               const int32_t* group_of, void* o, float* lse, StatusBlock* st, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.hq;
   // a row's partials are at most about its share of the workers: with as many rows as warps on the
   // GPU (148 x 8) one warp per row has enough loads in flight
   if (rows >= kCtas * kWarps)
     FPX_CHAIN((join_kernel<OT, D, 1>), static_cast<unsigned>((rows + 7) / 8), 256, 0, s, p, own,
-              shared, group_of, static_cast<OT*>(o), lse);
+              shared, group_of, static_cast<OT*>(o), lse, st);
   else
     FPX_CHAIN((join_kernel<OT, D, 8>), static_cast<unsigned>(rows), 256, 0, s, p, own, shared,
-              group_of, static_cast<OT*>(o), lse);
+              group_of, static_cast<OT*>(o), lse, st);
   return cudaGetLastError();
 }
 
@@ -1285,7 +1335,10 @@ cudaError_t launch_decode(const decode::DecodeDesc& p, fpx_dtype dt, const void*
     *encode_failed = true;
     return cudaErrorInvalidValue;
   }
-  FPX_CHAIN(plan_kernel, 1, kPlanThreads, 0, s, p, L.own, L.shared, group_of, st);
+  if (p.num_groups == 0 && p.num_seqs <= kLocalSeqs)
+    L.own.owners = nullptr;  // laid out by each CTA
+  else
+    FPX_CHAIN(plan_kernel, 1, kPlanThreads, 0, s, p, L.own, L.shared, group_of, st);
   cudaError_t e;
   if (p.num_groups > 0) {
     e = L.tc_shared ? launch_tc(p, L.shared, q, kc, vc, st, s, encode_failed)
@@ -1294,10 +1347,10 @@ cudaError_t launch_decode(const decode::DecodeDesc& p, fpx_dtype dt, const void*
   }
   if ((e = launch_line(mk, mv, p, dt, L.own, L.rw_own, q, st, s)) != cudaSuccess) return e;
   if (dt == FPX_F32)
-    return p.d == 128 ? launch_join<float, 128>(p, L.own, L.shared, group_of, o, lse, s)
-                      : launch_join<float, 64>(p, L.own, L.shared, group_of, o, lse, s);
-  return p.d == 128 ? launch_join<__nv_bfloat16, 128>(p, L.own, L.shared, group_of, o, lse, s)
-                    : launch_join<__nv_bfloat16, 64>(p, L.own, L.shared, group_of, o, lse, s);
+    return p.d == 128 ? launch_join<float, 128>(p, L.own, L.shared, group_of, o, lse, st, s)
+                      : launch_join<float, 64>(p, L.own, L.shared, group_of, o, lse, st, s);
+  return p.d == 128 ? launch_join<__nv_bfloat16, 128>(p, L.own, L.shared, group_of, o, lse, st, s)
+                    : launch_join<__nv_bfloat16, 64>(p, L.own, L.shared, group_of, o, lse, st, s);
 }
 
 }  // namespace fpx

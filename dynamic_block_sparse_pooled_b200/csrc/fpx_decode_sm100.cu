@@ -398,7 +398,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool valid = row < line.tpt * p.group && tk < w.tok1;
       const int head = w.kvh * p.group + row % p.group;
       RowPos rp = row_pos(p, valid ? tk : w.tok);
-      if (!valid) rp.span = {0, INT_MAX};  // discarded: no reason to mask
+      // rows of no query hold leftovers of shared memory: masked, they decide nothing for their warp
+      if (!valid) rp.span = {0, -1};
       rp.span.hi = min(rp.span.hi, w.k1 - 1);
       const ScoreMap map = score_map(p.rule, p.scale, head);
       TanhPoly poly = {};
@@ -519,6 +520,17 @@ void tc_line(const DecodeDesc& p, Line* l) {
   l->rps = 256;
 }
 
+template <bool kCap, bool kBias>
+static cudaError_t launch_tc_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const DecodeDesc& p, const Line& line, StatusBlock* st,
+                               cudaStream_t s) {
+  const cudaError_t e = allow_smem<decode_tc_kernel<kCap, kBias>>(kTcSmem);
+  if (e != cudaSuccess) return e;
+  FPX_CHAIN((decode_tc_kernel<kCap, kBias>), line.nw, kTcThreads, kTcSmem, s, mq, mk, mv, p, line,
+            st);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_tc(const DecodeDesc& p, const Line& line, const void* q, const void* kc,
                       const void* vc, StatusBlock* st, cudaStream_t s, bool* encode_failed) {
   CUtensorMap mq, mk, mv;
@@ -531,13 +543,10 @@ cudaError_t launch_tc(const DecodeDesc& p, const Line& line, const void* q, cons
     return cudaErrorInvalidValue;
   }
   const bool cap = p.rule.softcap > 0.f, bias = p.rule.slopes != nullptr;
-  auto kern = cap ? (bias ? decode_tc_kernel<true, true> : decode_tc_kernel<true, false>)
-                  : (bias ? decode_tc_kernel<false, true> : decode_tc_kernel<false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kTcSmem));
-  if (e != cudaSuccess) return e;
-  FPX_CHAIN(kern, line.nw, kTcThreads, kTcSmem, s, mq, mk, mv, p, line, st);
-  return cudaGetLastError();
+  return cap ? (bias ? launch_tc_t<true, true>(mq, mk, mv, p, line, st, s)
+                     : launch_tc_t<true, false>(mq, mk, mv, p, line, st, s))
+             : (bias ? launch_tc_t<false, true>(mq, mk, mv, p, line, st, s)
+                     : launch_tc_t<false, false>(mq, mk, mv, p, line, st, s));
 }
 
 }  // namespace decode

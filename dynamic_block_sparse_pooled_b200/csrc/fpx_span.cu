@@ -132,8 +132,7 @@ cudaError_t launch_span_count(const ProblemDesc& p, const RuleDesc& rule, SeqTab
   if (R == 0) return cudaSuccess;
   // nb_max <= 65535 (the worst-case CSR fits int32), so at most 64 KB
   const size_t smem = sizeof(uint32_t) * span::kWarps * static_cast<size_t>(mask_words);
-  cudaError_t e = cudaFuncSetAttribute(
-      span::span_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_smem<span::span_count_kernel>(64 * 1024);
   if (e != cudaSuccess) return e;
   FPX_CHAIN(span::span_count_kernel, static_cast<unsigned>((R + span::kWarps - 1) / span::kWarps),
             span::kWarps * 32, smem, s, p, rule, t, counts, cta_tot, mask, mask_words);

@@ -280,14 +280,12 @@ static cudaError_t launch_t(const ProblemDesc& p, const void* q, const void* k, 
                             const int32_t* row_ptr, const int32_t* col_idx, void* o, float* lse,
                             SeqTables t, const int32_t* order, const RuleDesc& rule,
                             StatusBlock* st, cudaStream_t s) {
-  auto kern = span_simt_kernel<T, OT, D, kRows>;
   constexpr size_t smem =
       sizeof(float) * (3 * kRows * (D + 4) + kRows * (kRows + 4) + kRows);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = allow_smem<span_simt_kernel<T, OT, D, kRows>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(p.hq) * p.nb_total * (p.block / kRows);
-  FPX_CHAIN(kern, static_cast<unsigned>(grid), kSimtThreads, smem, s, p,
+  FPX_CHAIN((span_simt_kernel<T, OT, D, kRows>), static_cast<unsigned>(grid), kSimtThreads, smem, s, p,
             static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), row_ptr,
             col_idx, static_cast<OT*>(o), lse, t, order, rule, st);
   return cudaGetLastError();
