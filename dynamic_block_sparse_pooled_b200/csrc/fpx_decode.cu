@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeDesc p, Line o
 }
 
 // Few requests and nothing shared: every CTA lays the line out for itself in shared memory instead of
-// waiting for a launch that does (one warp; 3 requests 19.5 -> see launch_decode).
+// waiting for a launch that does (one warp; replayed from a graph, 1 / 16 / 64 requests of 500 tokens: 14 /
+// 17 / 39 us instead of 16 / 21 / 49).
 constexpr int kLocalSeqs = 64;
 
 __device__ __forceinline__ void plan_local(const DecodeDesc& p, Line& l, Owner* owners,
@@ -1157,15 +1158,26 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
 
 // ---- host side --------------------------------------------------------------------------------------
 
-// Warps of a worker: enough 16-row tiles for the rows that share keys, so that they are read from
-// shared memory's one copy; up to a whole CTA.
+// Warps of a worker.  bf16: enough 16-row tiles for the rows that share keys, so that these are read
+// from one copy in shared memory; up to a whole CTA (8 requests at 8192 tokens, 32 / 64 / 128 / 256
+// rows per KV head: 74 / 125 / 217 / 421 us; with one warp 99 / 173 / 289 / 632, with eight 203 / 203
+// / 217 / 420).  e4m3: one.  There the conversions and products set the pace, not the reads, and a
+// worker of several warps pads its rows to more (same sizes: 75 / 127 / 237 / 453 us with one warp,
+// 80 / 139 / 242 / 476 by the bf16 rule).
+static int warps_for(int64_t rows, fpx_dtype dt) {
+  if (dt == FPX_E4M3) return 1;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
+}
+
 // What a segment costs a worker in itself, in key tiles.  Measured with 0 / 1 / 2 / 4 / 6: 48 requests
 // of 53 to 4220 keys on an e4m3 cache 129 / 105 / 102 / 106 / 106 us, 128 requests of 1 to 601 keys
 // behind a prompt 160 / 149 / 148 / 149 / 150 us; long contexts do not change.
 constexpr int kPad = 2, kPadTc = 2;
-// Rows (per group and KV head, on average) from which the shared part takes 128-row tiles.
+// Rows (per group and KV head, on average) from which the shared part takes 128-row tiles: behind a
+// prompt of 18944 tokens 32 / 48 / 64 / 128 / 256 rows take 57 / 58 / 60 / 73 / 78 us with them and
+// 51 / 67 / 68 / 99 / 162 us with 16-row tiles.
 constexpr int kTcRows = 48;
-static int warps_for(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+
 
 struct Layout {
   int rw_own, rw_shared;  // warps per worker (fp32: 1)
@@ -1183,8 +1195,8 @@ static Layout layout_of(const DecodeDesc& p, fpx_dtype dt) {
     L.own.rt = L.shared.rt = kRowsF32;
     L.own.tile = L.shared.tile = kTileF32;
   } else {
-    L.rw_own = warps_for(own_rows);
-    L.rw_shared = warps_for(p.num_groups > 0 ? (all_rows + p.num_groups - 1) / p.num_groups : 1);
+    L.rw_own = warps_for(own_rows, dt);
+    L.rw_shared = warps_for(p.num_groups > 0 ? (all_rows + p.num_groups - 1) / p.num_groups : 1, dt);
     L.own.rt = 16 * L.rw_own;
     L.shared.rt = 16 * L.rw_shared;
     L.own.tile = L.shared.tile = kTile;
@@ -1242,15 +1254,15 @@ static cudaError_t launch_mma_t(const CUtensorMap& mk, const CUtensorMap& mv, co
   return cudaGetLastError();
 }
 
-template <bool kFp8, int D>
-static cudaError_t launch_mma(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeDesc& p,
-                              const Line& line, int rw, const void* q, StatusBlock* st,
-                              cudaStream_t s) {
+template <int D>
+static cudaError_t launch_bf16(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeDesc& p,
+                               const Line& line, int rw, const void* q, StatusBlock* st,
+                               cudaStream_t s) {
   switch (rw) {
-    case 1: return launch_mma_t<kFp8, D, 1>(mk, mv, p, line, q, st, s);
-    case 2: return launch_mma_t<kFp8, D, 2>(mk, mv, p, line, q, st, s);
-    case 4: return launch_mma_t<kFp8, D, 4>(mk, mv, p, line, q, st, s);
-    default: return launch_mma_t<kFp8, D, 8>(mk, mv, p, line, q, st, s);
+    case 1: return launch_mma_t<false, D, 1>(mk, mv, p, line, q, st, s);
+    case 2: return launch_mma_t<false, D, 2>(mk, mv, p, line, q, st, s);
+    case 4: return launch_mma_t<false, D, 4>(mk, mv, p, line, q, st, s);
+    default: return launch_mma_t<false, D, 8>(mk, mv, p, line, q, st, s);
   }
 }
 
@@ -1275,18 +1287,19 @@ static cudaError_t launch_line(const CUtensorMap& mk, const CUtensorMap& mv, con
     return p.d == 128 ? launch_f32<128>(mk, mv, p, line, q, st, s)
                       : launch_f32<64>(mk, mv, p, line, q, st, s);
   if (dt == FPX_BF16)
-    return p.d == 128 ? launch_mma<false, 128>(mk, mv, p, line, rw, q, st, s)
-                      : launch_mma<false, 64>(mk, mv, p, line, rw, q, st, s);
-  return p.d == 128 ? launch_mma<true, 128>(mk, mv, p, line, rw, q, st, s)
-                    : launch_mma<true, 64>(mk, mv, p, line, rw, q, st, s);
+    return p.d == 128 ? launch_bf16<128>(mk, mv, p, line, rw, q, st, s)
+                      : launch_bf16<64>(mk, mv, p, line, rw, q, st, s);
+  return p.d == 128 ? launch_mma_t<true, 128, 1>(mk, mv, p, line, q, st, s)
+                    : launch_mma_t<true, 64, 1>(mk, mv, p, line, q, st, s);
 }
 
 template <typename OT, int D>
 static cudaError_t launch_join(const DecodeDesc& p, const Line& own, const Line& shared,
                                const int32_t* group_of, void* o, float* lse, StatusBlock* st, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.hq;
-  // a row's partials are at most about its share of the workers: with as many rows as warps on the
-  // GPU (148 x 8) one warp per row has enough loads in flight
+  // With as many rows as warps on the GPU one warp per row keeps enough loads in flight (2048 / 8192
+  // rows: 183 / 208 us a call with one, 190 / 237 with eight); with fewer, the chain over a row's
+  // partials counts (32 / 128 rows: 126 / 64 us with one, 101 / 57 with eight).
   if (rows >= kCtas * kWarps)
     FPX_CHAIN((join_kernel<OT, D, 1>), static_cast<unsigned>((rows + 7) / 8), 256, 0, s, p, own,
               shared, group_of, static_cast<OT*>(o), lse, st);

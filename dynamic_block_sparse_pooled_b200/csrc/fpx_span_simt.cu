@@ -7,7 +7,8 @@
 // shared memory, transposed, so that P V has a thread at 4 rows x 4 or 8 columns (3 loads for 32
 // multiply-adds).  The next keys are loaded into registers while the present ones are used.  Small
 // row tiles, because what runs here is short: a 1000-token layer of 2 heads has 64 CTAs.
-// (1000 tokens, 2 heads, D 64, window 200: see the measurement at launch_span_simt.)
+// 1000 tokens, 2 heads, D 64, window 200, the pass with spans and selection: 46 us, 175 us with a thread
+// per query row.  What bounds it is the chain of short launches and, inside, latency.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
