@@ -527,6 +527,14 @@ def _call(name: str, device: int, stream, *args) -> None:
         raise FpxError(code, name)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a launch on `stream`: its memory belongs to that stream's pool."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def score_rule(softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
                key_lo: Optional[torch.Tensor] = None,
                key_hi: Optional[torch.Tensor] = None) -> ScoreRule:
@@ -565,8 +573,8 @@ def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
         raise ValueError("doc_cu needs at least one document")
     _expect("doc_cu", doc_cu, torch.int32, dev)
     _expect("prefix", prefix, torch.int32, dev, docs if doc_cu is not None else pf.struct.num_seqs)
-    key_lo = torch.empty(total, dtype=torch.int32, device=on) if key_lo is None else key_lo
-    key_hi = torch.empty(total, dtype=torch.int32, device=on) if key_hi is None else key_hi
+    key_lo = _empty(total, torch.int32, on, stream) if key_lo is None else key_lo
+    key_hi = _empty(total, torch.int32, on, stream) if key_hi is None else key_hi
     _expect("key_lo", key_lo, torch.int32, dev, total)
     _expect("key_hi", key_hi, torch.int32, dev, total)
     _call("fpx_spans", dev, stream, pf.ptr, docs, _ptr(doc_cu), _ptr(prefix), _ptr(key_lo),
@@ -589,13 +597,16 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
     _expect("ws", ws, torch.uint8, index)
     _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, index)
     if row_ptr is None:
-        row_ptr = torch.empty(pf.rows + 1, dtype=torch.int32, device=dev)
+        row_ptr = _empty(pf.rows + 1, torch.int32, dev, stream)
     if col_idx is None:
-        cap = span_capacity(pf) if capacity is None else capacity
-        col_idx = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
+        if capacity is not None:
+            cap = capacity
+        else:  # without key spans no block lies above the diagonal
+            cap = span_capacity(pf) if rule.key_lo_d else pf.struct.hq * pf.tri
+        col_idx = _empty(max(cap, 1), torch.int32, dev, stream)
     cap = col_idx.numel() if capacity is None else capacity
     if nnz is None:
-        nnz = torch.empty(1, dtype=torch.int64, device=dev)
+        nnz = _empty(1, torch.int64, dev, stream)
     _check_csr_outputs(pf, row_ptr, col_idx, nnz, cap)
     _call("fpx_span_select", index, stream, pf.ptr, ctypes.byref(rule), _ptr(row_ptr),
           _ptr(col_idx), cap, _ptr(nnz), _ptr(ws), ws.numel())
@@ -621,9 +632,9 @@ def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _expect("row_ptr", row_ptr, torch.int32, dev, pf.rows + 1)
     _expect("col_idx", col_idx, torch.int32, dev)
     odt = torch.float32 if q.dtype == torch.float32 else torch.bfloat16
-    o = torch.empty(q.shape, dtype=odt, device=q.device) if o is None else o
+    o = _empty(q.shape, odt, q.device, stream) if o is None else o
     if lse is None and want_lse:
-        lse = torch.empty((p.hq, p.total_tokens), dtype=torch.float32, device=q.device)
+        lse = _empty((p.hq, p.total_tokens), torch.float32, q.device, stream)
     _expect("o", o, odt, dev, shape=q.shape)
     _expect("lse", lse, torch.float32, dev, p.hq * p.total_tokens)
     _expect("ws", ws, torch.uint8, dev)
@@ -674,11 +685,11 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
         raise ValueError("block_table must be [num_seqs, pages_per_seq]")
     i32 = torch.int32
     if cu_new is None:
-        cu_new = torch.empty(n + 1, dtype=i32, device=lens.device)
+        cu_new = _empty(n + 1, i32, lens.device, stream)
     if slots is None:
-        slots = torch.empty(token_capacity, dtype=i32, device=lens.device)
+        slots = _empty(token_capacity, i32, lens.device, stream)
     if positions is None:
-        positions = torch.empty(token_capacity, dtype=i32, device=lens.device)
+        positions = _empty(token_capacity, i32, lens.device, stream)
     _expect("lens", lens, i32, dev)
     _expect("new_lens", new_lens, i32, dev, n)
     _expect("keep_pages", keep_pages, i32, dev, n)
@@ -810,13 +821,13 @@ def decode(dp: Decode, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if rule is not None:
         _check_rule(rule, p.hq, tokens, dev)
     if o is None:
-        o = torch.empty(dp.q_shape, dtype=dp.q_dtype, device=dp.device)
+        o = _empty(dp.q_shape, dp.q_dtype, dp.device, stream)
     else:
         _expect("o", o, dp.q_dtype, dev, shape=dp.q_shape)
     if lse is not None:
         _expect("lse", lse, torch.float32, dev, p.hq * tokens)
     elif want_lse:
-        lse = torch.empty((p.hq, tokens), dtype=torch.float32, device=dp.device)
+        lse = _empty((p.hq, tokens), torch.float32, dp.device, stream)
     _expect("ws", ws, torch.uint8, dev)
     _call("fpx_decode", dev, stream, dp.ptr, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           ctypes.byref(rule) if rule is not None else None, o.data_ptr(), _ptr(lse),

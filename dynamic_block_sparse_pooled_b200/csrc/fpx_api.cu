@@ -102,7 +102,8 @@ fpx_status apply_paged(const fpx_problem* p, const Sizes& s, const fpx_paged_kv*
 
 // Host checks of a score rule; fills the kernels' form.
 fpx_status check_rule(const fpx_score_rule* r, RuleDesc* d) {
-  if (!std::isfinite(r->softcap) || r->softcap < 0.f || r->window < 0) return FPX_ERR_INVALID_ARG;
+  if (!(r->softcap == 0.f || (r->softcap >= 1e-20f && r->softcap <= 1e20f)) || r->window < 0)
+    return FPX_ERR_INVALID_ARG;
   if ((r->key_lo_d == nullptr) != (r->key_hi_d == nullptr)) return FPX_ERR_INVALID_ARG;
   if (!aligned(r->slopes_d, 4) || !aligned(r->key_lo_d, 4) || !aligned(r->key_hi_d, 4))
     return FPX_ERR_ALIGNMENT;

@@ -614,7 +614,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              s[nt][k] = map[k >> 1].cap2 * tanh_ex2(s[nt][k] * map[k >> 1].k);
+              s[nt][k] = map[k >> 1].cap2 * tanh_any(s[nt][k] * map[k >> 1].k);
         }
         if (biased) {
           const float rel[2] = {static_cast<float>(R.pos[0] - kb - (kFp8 ? 0 : c4 * 2)),

@@ -37,10 +37,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error a few 2^-23 for any x, which is what a
-// score needs (it is scaled by the cap and then exponentiated).
+// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error a few 2^-23 for any x.  Enough for a score
+// where x is not small, as the error is then small against the score too.
 __device__ __forceinline__ float tanh_ex2(float x) {
   return fmaf(-2.f, rcp_approx(1.f + ex2_approx(x * 2.8853900817779268f)), 1.f);
+}
+// The same with a small relative error for small x (scores far below the cap, whatever the cap): the
+// series to x^7 below 1/5, its next term 6e-8 of the sum there.
+__device__ __forceinline__ float tanh_any(float x) {
+  const float u = x * x;
+  const float p = fmaf(fmaf(fmaf(-17.f / 315.f, u, 2.f / 15.f), u, -1.f / 3.f), u, 1.f);
+  return u < 0.04f ? x * p : tanh_ex2(x);
 }
 
 // Scores in log2 units from raw dot products: scale, cap, distance bias.
@@ -50,7 +57,7 @@ struct ScoreMap {
   float slope2; // slopes[h] * log2 e; 0: no bias
   __device__ __forceinline__ float operator()(float dot, float dist) const {
     float y = dot * k;
-    if (cap2 != 0.f) y = cap2 * tanh_ex2(y);
+    if (cap2 != 0.f) y = cap2 * tanh_any(y);
     return fmaf(-slope2, dist, y);
   }
 };

@@ -286,7 +286,7 @@ fpx_status fpx_vs_prefill(const fpx_problem* p, const void* q, const void* k, co
  * seen may be anything, NaN included.
  */
 typedef struct {
-  float softcap;           /* 0: none; finite, >= 0                                            */
+  float softcap;           /* 0: none; else in [1e-20, 1e20]                                   */
   int32_t window;          /* 0: none; the last `window` positions up to the query's own       */
   const float* slopes_d;   /* device fp32 [hq], or NULL                                        */
   const int32_t* key_lo_d; /* device int32 [query tokens], or NULL; both or neither            */

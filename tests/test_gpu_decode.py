@@ -123,7 +123,7 @@ def test_heads_and_drafts(dtype, hq, hkv, q_len):
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
 @pytest.mark.parametrize("rule", [dict(softcap=7.0), dict(slopes=True), dict(window=1),
                                   dict(window=50), dict(softcap=4.0, slopes=True, window=333),
-                                  dict(window=2 ** 31 - 1)])
+                                  dict(window=2 ** 31 - 1), dict(softcap=1e5), dict(softcap=1e-3)])
 @pytest.mark.parametrize("grouped", [False, True])
 def test_rules(dtype, rule, grouped):
     groups = dict(groups=[0, 4, 4, 7], prefix=[3, 2, 9]) if grouped else {}
@@ -170,6 +170,7 @@ PROMPTS = {
     "window behind": (8, 2, 64, 40, 1, 20, dict(window=5)),
     "cap": (8, 2, 128, 50, 1, 9, dict(softcap=6.0)),
     "cap far": (8, 2, 128, 30, 1, 9, dict(softcap=0.5)),
+    "cap above": (8, 2, 128, 30, 1, 9, dict(softcap=1e5)),
     "bias": (8, 2, 32, 50, 1, 9, dict(slopes=True)),
     "cap bias window": (6, 2, 16, 45, 2, 70, dict(softcap=9.0, slopes=True, window=900)),
 }

@@ -105,6 +105,13 @@ def test_cap_at_its_ends(gain):
     run("simt_f32", [200], softcap=8.0, gain=gain)
 
 
+@pytest.mark.parametrize("shape", ["tc_gqa2", "simt_f32", "tc_e4m3"])
+@pytest.mark.parametrize("cap", [1e-3, 3e3, 1e6])
+def test_caps_far_from_the_scores(shape, cap):
+    """A cap far above the scores leaves them as they are, one far below makes them signs of it."""
+    run(shape, [300, 129], softcap=cap)
+
+
 @pytest.mark.parametrize("block", [16, 128])
 @pytest.mark.parametrize("rule", sorted(RULES))
 def test_blocks_listed(rule, block):
@@ -279,3 +286,30 @@ def test_captured_and_replayed_with_other_spans():
         go()
         assert fpx.status(ws) == 0
         assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
+def test_default_capacity_and_another_stream():
+    """Lists of the default size hold a rule without spans (on or below the diagonal) and one with
+    them; outputs allocated for another stream."""
+    (q, k, v), (q64, k64, v64), _ = make("bf16", [700], 2, 1, 128)
+    pf = fpx.problem(q, k, 128)
+    s = torch.cuda.Stream()
+    ws = fpx.workspace(pf, -1)
+    s.wait_stream(torch.cuda.current_stream())
+    plain = fpx.score_rule(window=300)
+    rp, ci, nnz = fpx.span_select(pf, plain, ws, stream=s)
+    assert ci.numel() == 2 * 21
+    o, lse = fpx.span_prefill(pf, q, k, v, plain, rp, ci, ws, stream=s)
+    lo, hi = fpx.spans(pf, None, torch.tensor([700], dtype=torch.int32, device="cuda"), stream=s)
+    s.wait_stream(torch.cuda.current_stream())
+    both = fpx.score_rule(key_lo=lo, key_hi=hi)
+    rp2, ci2, _ = fpx.span_select(pf, both, ws, stream=s)
+    o2, lse2 = fpx.span_prefill(pf, q, k, v, both, rp2, ci2, ws, stream=s)
+    assert fpx.status(ws, s) == 0 and ci2.numel() == 2 * 36
+    torch.cuda.synchronize()
+    a, b = R.span_bounds([700])
+    R.check(o, lse, R.span_reference(q64, k64, v64, [700], a, b, 1 / math.sqrt(128), window=300),
+            "bf16", "bf16", 700, 128)
+    a, b = R.span_bounds([700], None, [700])
+    R.check(o2, lse2, R.span_reference(q64, k64, v64, [700], a, b, 1 / math.sqrt(128)), "bf16",
+            "bf16", 700, 128)

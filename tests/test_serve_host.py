@@ -28,7 +28,8 @@ def rule(softcap=0.0, window=0, slopes=None, lo=None, hi=None):
 
 BAD_RULES = {
     "negative cap": (dict(softcap=-1.0), -1), "nan cap": (dict(softcap=float("nan")), -1),
-    "infinite cap": (dict(softcap=float("inf")), -1), "negative window": (dict(window=-1), -1),
+    "infinite cap": (dict(softcap=float("inf")), -1), "cap below its range": (dict(softcap=1e-30), -1),
+    "cap beyond its range": (dict(softcap=1e30), -1), "negative window": (dict(window=-1), -1),
     "lo alone": (dict(lo=A), -1), "hi alone": (dict(hi=A), -1),
     "slopes misaligned": (dict(slopes=A + 2), -3), "lo misaligned": (dict(lo=A + 1, hi=A), -3),
 }
