@@ -57,7 +57,7 @@ struct ScoreMap {
   float slope2; // slopes[h] * log2 e; 0: no bias
   __device__ __forceinline__ float operator()(float dot, float dist) const {
     float y = dot * k;
-    if (cap2 != 0.f) y = cap2 * tanh_any(y);
+    if (cap2 != 0.f) y = cap2 * tanhf(y);  // the 32-bit kernels: to the last bits
     return fmaf(-slope2, dist, y);
   }
 };
