@@ -47,9 +47,9 @@ ATTN_SOURCES = ("dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cu",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_softmax.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_sm100.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_common.cuh")
-ATTN_TRAFFIC_DIGEST = "c164f9110e1aa5b205955d689f88dda2d0ae3296ffaf1cdf2e200962ca78dbe8"
+ATTN_TRAFFIC_DIGEST = "a3978d45273cf2bed10370f18451224d9ea417207bc35772aac5243e97c895d5"
 ATTN_TRAFFIC = {
-    "llama8b_bf16_n131072": 3305845760 + 1181199872,
+    "llama8b_bf16_n131072": 3299498240 + 1179589376,
 }
 
 

@@ -684,12 +684,6 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table must be [num_seqs, pages_per_seq]")
     i32 = torch.int32
-    if cu_new is None:
-        cu_new = _empty(n + 1, i32, lens.device, stream)
-    if slots is None:
-        slots = _empty(token_capacity, i32, lens.device, stream)
-    if positions is None:
-        positions = _empty(token_capacity, i32, lens.device, stream)
     _expect("lens", lens, i32, dev)
     _expect("new_lens", new_lens, i32, dev, n)
     _expect("keep_pages", keep_pages, i32, dev, n)
@@ -697,10 +691,19 @@ def page_resize(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     _expect("free_pages", free_pages, i32, dev, num_pages)
     _expect("free_count", free_count, i32, dev, 1)
     _expect("count_out", count_out, i32, dev, 1)
-    _expect("cu_new", cu_new, i32, dev, n + 1)
-    _expect("slots", slots, i32, dev, token_capacity)
-    _expect("positions", positions, i32, dev, token_capacity)
     _expect("ws", ws, torch.uint8, dev)
+    if cu_new is None:
+        cu_new = _empty(n + 1, i32, lens.device, stream)
+    else:
+        _expect("cu_new", cu_new, i32, dev, n + 1)
+    if slots is None:
+        slots = _empty(token_capacity, i32, lens.device, stream)
+    else:
+        _expect("slots", slots, i32, dev, token_capacity)
+    if positions is None:
+        positions = _empty(token_capacity, i32, lens.device, stream)
+    else:
+        _expect("positions", positions, i32, dev, token_capacity)
     _call("fpx_page_resize", dev, stream, n, page, num_pages, lens.data_ptr(),
           new_lens.data_ptr(), _ptr(keep_pages), block_table.data_ptr(), block_table.shape[1],
           free_pages.data_ptr(), free_count.data_ptr(), count_out.data_ptr(), cu_new.data_ptr(),

@@ -209,8 +209,10 @@ __device__ __forceinline__ void bits128(const uint32_t* __restrict__ row, int wo
 // listed blocks may lie above the diagonal.  The rule's transform runs on the S row in registers
 // between the TMEM load and the row maximum.  kRules says which parts the rule has, so that a layer
 // without a cap or a bias does not carry their code through the row loop: bit 0 a rule, bit 1 a
-// cap, bit 2 a distance bias.  (The instantiations are spread over
-// several files: each takes long to compile.)
+// cap, bit 2 a distance bias.  (8192 tokens, 32 heads: no rule 467 us, cap 640; 13875 tokens in
+// documents with prefixes, 16 heads: spans alone 181 us, with a bias 236; one kernel with run-time
+// switches took 285 there.  The instantiations are spread over several files, as each takes long to
+// compile.)
 template <bool kFp8, bool kMask, int kRules>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

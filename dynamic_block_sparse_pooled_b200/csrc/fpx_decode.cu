@@ -2,9 +2,10 @@
 // shared by groups of requests read once per group.
 //
 // Bound by HBM: each cached K / V row is read once per (request or group) and used for q_len x
-// group rows.  A worker (one warp for up to 16 rows, 2, 4 or 8 warps for more) owns a ring in
-// shared memory that it fills itself with TMA, K and V half-stages of 32 keys alternating, so it
-// never waits for another worker; the eight warps of a CTA keep up to 192 KB in flight per SM.
+// group rows (one request of 131072 tokens, 8 KV heads, bf16: 537 MB in 87 us, 6.1 TB/s).  A worker
+// (one warp; for bf16 and more than 16 rows 2, 4 or 8) owns a ring in shared memory that it fills
+// itself with TMA, K and V half-stages of 32 keys alternating, so it never waits for another worker;
+// the eight warps of a CTA keep up to 192 KB in flight per SM.
 // The products run on mma.sync m16n8k16: 16 rows is the least a tensor instruction takes and
 // most batches fill only group x q_len of them, so the tensor pipe is far from the limit and a
 // 128-row tcgen05 tile would only add latency.
@@ -14,7 +15,9 @@
 //               2^-14 of it), P in f16, the head's scales in 32 bits outside the products.  K^T and V
 //               fragments are read by plain 16-byte shared loads: the order of the D dimension
 //               (for K) and of the keys in eights is permuted alike on both operands, so that each
-//               lane's bytes are contiguous and free of bank conflicts.
+//               lane's bytes are contiguous and free of bank conflicts.  Bound by instruction issue
+//               (128 conversions, 64 permutes, 64 products per 32 keys): 138 MB in 42 us, 3.3 TB/s;
+//               widening by integer operations was 20 % slower, 64 keys a tile the same.
 //   fp32 cache  CUDA cores, all 32-bit: a lane per key for the scores, a lane per four
 //               dimensions for P V.
 #include <cuda.h>

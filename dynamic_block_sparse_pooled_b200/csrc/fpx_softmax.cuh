@@ -81,10 +81,9 @@ __device__ __forceinline__ float softmax_part_to_p(uint32_t* r, float sl2, float
   return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-// Columns [J0, J0 + N) of raw capped scores, all within kTanhNear of the cap, become P: tanh as
-// x (c0 + c1 x^2 + c2 x^4 + c3 x^6) (largest absolute error 1.6e-7 for |x| <= 1/2, fitted
-// by tanh_poly_fit.py), the
-// maximum subtracted by the last multiply-add.  Four pairs at a time, stage by stage: eight
+// Columns [J0, J0 + N) of raw capped scores, all at most kTanhNear of the cap, become P: tanh as
+// x (c0 + c1 x^2 + c2 x^4 + c3 x^6) (largest absolute error 1.6e-7 for |x| <= 1/2, fitted by
+// tanh_poly_fit.py), the maximum subtracted by the last multiply-add.  Four pairs at a time, stage by stage: eight
 // independent values hide the latency of the chain, which one warp per SM sub-partition and tile
 // otherwise waits for (8192 tokens, 32 heads: two pairs at a time 719 us, four 660, eight 659).
 constexpr float kTanhNear = 0.5f;
