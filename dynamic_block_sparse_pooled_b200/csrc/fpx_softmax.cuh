@@ -82,13 +82,13 @@ __device__ __forceinline__ float softmax_part_to_p(uint32_t* r, float sl2, float
 }
 
 // Columns [J0, J0 + N) of raw capped scores, all at most kTanhNear of the cap, become P: tanh as
-// x (c0 + c1 x^2 + c2 x^4 + c3 x^6) (largest absolute error 1.6e-7 for |x| <= 1/2, fitted by
+// x (c0 + c1 x^2 + c2 x^4 + c3 x^6) (largest relative error 6.2e-7 for |x| <= 1/2, fitted by
 // tanh_poly_fit.py), the maximum subtracted by the last multiply-add.  Four pairs at a time, stage by stage: eight
 // independent values hide the latency of the chain, which one warp per SM sub-partition and tile
 // otherwise waits for (8192 tokens, 32 heads: two pairs at a time 719 us, four 660, eight 659).
 constexpr float kTanhNear = 0.5f;
-constexpr float kNear0 = 9.999976754e-01f, kNear1 = -3.332065642e-01f,
-                kNear2 = 1.314514577e-01f, kNear3 = -4.337247461e-02f;
+constexpr float kNear0 = 9.999994636e-01f, kNear1 = -3.332631886e-01f,
+                kNear2 = 1.319029629e-01f, kNear3 = -4.440220818e-02f;
 struct NearTanh {
   float c[4];
 };

@@ -1,10 +1,11 @@
 """Fits the polynomials behind the FMA-pipe tanh of capped attention scores (TanhPoly in
-fpx_sm100.cuh, NearTanh in fpx_attn_sm100.cu) and prints their coefficients and error bounds.
+fpx_sm100.cuh, NearTanh in fpx_softmax.cuh) and prints their coefficients and error bounds.
 
-Method: tanh(x) = x P(x^2) on [0, HI] with the smallest maximum *absolute* error (an error in a score
-is an absolute one), found by Lawson's iteration: least squares on a dense grid, the weights
-multiplied by the errors until these equioscillate.  The coefficients are then rounded to fp32 and
-the error of an fp32 evaluation is measured.
+Method: tanh(x) = x P(x^2) on [0, HI] with the smallest maximum *relative* error, found by Lawson's
+iteration: least squares on a dense grid, the weights multiplied by the errors until these
+equioscillate.  (The smallest absolute error would leave P(0) 2.3e-6 off for degree 3, and a score
+far below its cap with it: its absolute error is that times the score, whatever the cap.)  The
+coefficients are then rounded to fp32 and the error of an fp32 evaluation is measured.
 
     python dynamic_block_sparse_pooled_b200/csrc/tanh_poly_fit.py
 """
@@ -13,13 +14,13 @@ import numpy as np
 
 def fit(deg, hi, iters=400):
     x = hi * np.sin(np.linspace(0, np.pi / 2, 4001)[1:])
-    basis = np.stack([x ** (2 * j + 1) for j in range(deg + 1)], axis=1)
+    basis = np.stack([x ** (2 * j + 1) / np.tanh(x) for j in range(deg + 1)], axis=1)
     w = np.full(len(x), 1.0 / len(x))
     best, best_err = None, np.inf
     for _ in range(iters):
         sw = np.sqrt(w)
-        c = np.linalg.lstsq(basis * sw[:, None], np.tanh(x) * sw, rcond=None)[0]
-        err = np.abs(basis @ c - np.tanh(x))
+        c = np.linalg.lstsq(basis * sw[:, None], sw, rcond=None)[0]
+        err = np.abs(basis @ c - 1.0)
         if err.max() < best_err:
             best, best_err = c, err.max()
         w = w * err
@@ -36,6 +37,8 @@ if __name__ == "__main__":
         p = np.full_like(g, c32[deg])
         for k in range(deg - 1, -1, -1):
             p = (p.astype(np.float64) * u + c32[k]).astype(np.float32)  # as a fused multiply-add
-        err = np.abs((p * g).astype(np.float64) - np.tanh(g.astype(np.float64)))
+        exact = np.tanh(g[1:].astype(np.float64))
+        err = np.abs((p * g)[1:].astype(np.float64) - exact)
         print(name, ", ".join(f"{float(v):.9e}f" for v in c32))
-        print(f"  max absolute error on [0, {hi}]: {e:.2e}, evaluated in fp32: {err.max():.2e}")
+        print(f"  max relative error on [0, {hi}]: {e:.2e}, evaluated in fp32: "
+              f"{(err / exact).max():.2e} (absolute {err.max():.2e})")

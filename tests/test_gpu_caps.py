@@ -1,0 +1,79 @@
+"""Attention under a tanh cap where the cap is far above the scores, up to the end of its range.
+
+Q and K are small whole numbers, so every dot product is exact in 32 bits and what is left of a
+score's error is known: the roundings of scale / cap, of the product with it, of cap log2 e and of
+the coefficients that it is folded into, and of the result (6 in all, counted as 8 half steps of
+2^-24), and the tanh polynomials' relative error (the largest, 6.2e-7, is that of the fit to 1/2;
+counted as POLY).  A row's LSE is off by at most that of its largest score, a weight by twice that.
+On top come the sum over n keys in 32 bits, the exponentials and logarithm (2^-20), and for O the
+roundings of P and of O itself as in serve_ref."""
+import math
+
+import pytest
+import torch
+
+import dynamic_block_sparse_pooled_b200 as fpx
+import serve_ref as R
+
+pytestmark = pytest.mark.gpu
+
+POLY = 7e-7
+SCALE = 16.0  # scores of some hundreds from dot products of some tens
+
+
+def whole(n, h, d, most, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-most, most + 1, (n, h, d), generator=g).double()
+
+
+def inputs(n, hq, hkv, shift, seed):
+    """q, k, v in 64 bits; the scores lie around shift * SCALE."""
+    q, k = whole(n, hq, 128, 2, seed), whole(n, hkv, 128, 1, seed + 1)
+    if shift:
+        q[..., 0], k[..., 0] = 8.0, shift / 8.0
+    v = torch.randn(n, hkv, 128, generator=torch.Generator().manual_seed(seed + 2))
+    return q, k, v.bfloat16().double()
+
+
+def close(o, lse, ref, scores, p_type):
+    """scores [Hq, n]: each row's largest |score|."""
+    o64, l64, a, _ = ref
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    err = scores.double() * (POLY + 8 * 2.0 ** -24)
+    lse_tol = err + o64.shape[0] * 2.0 ** -24 + 2.0 ** -20
+    worst = ((lse.double().cpu() - l64).abs() / lse_tol).max().item()
+    assert worst <= 1.0, f"LSE off by {worst:.2f} of its tolerance"
+    rel = R.P_STEP[p_type] + 2.0 ** -8 + 2.0 ** -10 + torch.expm1(2 * err).T[..., None]
+    tol = rel * a + R.P_LEAST[p_type] * ref[3] + 1e-6
+    worst = ((o.double().cpu() - o64).abs() / tol).max().item()
+    assert worst <= 1.0, f"O off by {worst:.2f} of its tolerance"
+
+
+def causal(q, k, v, cap):
+    n, hq = q.shape[:2]
+    at = torch.arange(n)
+    ref = R.attend(q, k, v, at, torch.zeros_like(at), at, SCALE, cap)
+    s = torch.einsum("nhd,lhd->hnl", q, k.repeat_interleave(hq // k.shape[1], dim=1)) * SCALE
+    s = torch.where(at[None, :] <= at[:, None], cap * torch.tanh(s.abs() / cap), torch.zeros(()).double())
+    return ref, s.amax(-1)
+
+
+def prefill(q, k, v, cap, dtype):
+    dt = torch.float8_e4m3fn if dtype == "e4m3" else torch.bfloat16
+    scales = {}
+    if dtype == "e4m3":
+        scales = {x + "_scale": torch.ones(t.shape[1], device="cuda") for x, t in (("q", q), ("k", k), ("v", v))}
+    dev = [x.float().to(dt).cuda() for x in (q, k, v)]
+    out = fpx.span_path(*dev, 128, softcap=cap, softmax_scale=SCALE, **scales)
+    return out["o"], out["lse"], dev[2].double().cpu()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shift", [0, -64, 64])
+@pytest.mark.parametrize("cap", [1e4, 1e5, 1e6])
+def test_scores_keep_their_relative_precision(dtype, shift, cap):
+    """Scores of hundreds (and around +-1024) far below the cap."""
+    q, k, v = inputs(640, 2, 1, shift, 5)
+    o, lse, v = prefill(q, k, v, cap, dtype)
+    ref, top = causal(q, k, v, cap)
+    close(o, lse, ref, top, dtype)
