@@ -694,9 +694,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tmem_wait_ld(r + 64);
           tmem_wait_ld(r + 96);
           const float mx = fmaxf(mx_lo, row_max64(r + 64)), mn = fminf(mn_lo, row_min64(r + 64));
+          // formed ahead of the vote: its chain overlaps it (660 us at 8192 tokens, behind it 709)
+          const float top = near(mx * map.k);
           if (__all_sync(kFull, fmaxf(mx, -mn) * map.k <= kTanhNear)) {
             redo = false;
-            rescale_to(map.cap2 * tanh_ex2(mx * map.k));
+            rescale_to(top);
             rs = capped_part_to_p<kFp8, 0, 64>(r, map.k, near, -m_ref);
             if (kFp8) tmem_st16(tS, r);
             else tmem_st32(tS, r);

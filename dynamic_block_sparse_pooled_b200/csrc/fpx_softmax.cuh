@@ -90,7 +90,14 @@ constexpr float kTanhNear = 0.5f;
 constexpr float kNear0 = 9.999994636e-01f, kNear1 = -3.332631886e-01f,
                 kNear2 = 1.319029629e-01f, kNear3 = -4.440220818e-02f;
 struct NearTanh {
-  float c[4];
+  float c[4];  // with the factor cap log2 e
+  // The score of x = dot / cap, by the operations that capped_part_to_p forms its weight's exponent
+  // with: the reference that the weights are taken against has to be one of their own scores, as any
+  // other form of tanh is off by its error times the cap.
+  __device__ __forceinline__ float operator()(float x) const {
+    const float u = x * x;
+    return x * fmaf(fmaf(fmaf(c[3], u, c[2]), u, c[1]), u, c[0]);
+  }
 };
 template <bool kFp8, int J0, int N>
 __device__ __forceinline__ float capped_part_to_p(uint32_t* r, float k, const NearTanh& th,

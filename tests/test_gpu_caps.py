@@ -77,3 +77,12 @@ def test_scores_keep_their_relative_precision(dtype, shift, cap):
     o, lse, v = prefill(q, k, v, cap, dtype)
     ref, top = causal(q, k, v, cap)
     close(o, lse, ref, top, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shift", [0, -64, 64])
+@pytest.mark.parametrize("cap", [1e8, 1e10, 1e15, 1e20])
+def test_caps_to_the_end_of_their_range(dtype, shift, cap):
+    """The reference that the weights are taken against must be that of the same scores: any other
+    one is off by its error times the cap."""
+    test_scores_keep_their_relative_precision(dtype, shift, cap)
