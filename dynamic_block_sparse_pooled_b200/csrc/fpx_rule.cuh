@@ -37,8 +37,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error a few 2^-23 for any x.  Enough for a score
-// where x is not small, as the error is then small against the score too.
+// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error at most 4e-7 for any x (with e = 2^(..), the
+// quotient q = 2 / (1 + e) <= 2 has the relative errors 2^-22 e / (1 + e) of ex2, 2^-24 of the sum and
+// 2^-23 of rcp; the exponent's own rounding, |2 x log2 e| 2^-24, is damped by e / (1 + e) or by q, and
+// 2^-25 for the result).  Enough for a score where x is not small, as the error is then small
+// against the score too.
 __device__ __forceinline__ float tanh_ex2(float x) {
   return fmaf(-2.f, rcp_approx(1.f + ex2_approx(x * 2.8853900817779268f)), 1.f);
 }

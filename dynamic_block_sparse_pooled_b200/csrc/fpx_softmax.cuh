@@ -141,6 +141,10 @@ __device__ __forceinline__ float capped_part_to_p(uint32_t* r, float k, const Ne
   return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
+// Largest cap (log2 units) whose scores may all take tanh_ex2: 4e-7 of it is 2e-4, a tenth of a
+// bf16 weight's rounding.
+constexpr float kEx2Cap = 512.f;
+
 // 64 columns of a row of S, the first of them column j0 of its key block, under a score rule: cap,
 // distance bias (rel = the row's position - the block's first key) and mask (columns [c_lo, c_hi] are
 // seen; partial: some row of the warp does not see all of the block before (bit 0) or behind (bit 1)
@@ -153,7 +157,11 @@ __device__ __forceinline__ void rule_half(uint32_t* x, int j0, const ScoreMap& m
   constexpr unsigned kFull = 0xffffffffu;
   if (kCap) {
     // Capped scores mostly lie well within the cap, where tanh is a polynomial on the
-    // FMA pipe; a warp with a score beyond that takes 2^x and a reciprocal on the MUFU.
+    // FMA pipe; a warp with a score beyond that takes 2^x and a reciprocal on the MUFU.  That form's
+    // error is absolute, 4e-7 of the cap: for all of the warp's scores where the cap is at most
+    // kEx2Cap, for those beyond alone where it is larger, as a score far below its cap would not
+    // keep its precision (per-score choice: 8192 tokens, cap 50, every warp with such a score, 1525 us
+    // instead of 1360).
     // Only seen scores count, so that no result depends on an unseen one.
     float top[4] = {0.f, 0.f, 0.f, 0.f};
     if (partial & 1) {
@@ -179,10 +187,19 @@ __device__ __forceinline__ void rule_half(uint32_t* x, int j0, const ScoreMap& m
         x[j] = __float_as_uint(x0);
         x[j + 1] = __float_as_uint(x1);
       }
-    } else {
+    } else if (map.cap2 <= kEx2Cap) {
 #pragma unroll
       for (int j = 0; j < 64; ++j)
         x[j] = __float_as_uint(map.cap2 * tanh_ex2(__uint_as_float(x[j]) * map.k));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 64; j += 2) {
+        float x0 = __uint_as_float(x[j]), x1 = __uint_as_float(x[j + 1]);
+        const float t0 = x0 * map.k, t1 = x1 * map.k;
+        poly(x0, x1, map.k);
+        x[j] = __float_as_uint(fabsf(t0) <= TanhPoly::kMost ? x0 : map.cap2 * tanh_ex2(t0));
+        x[j + 1] = __float_as_uint(fabsf(t1) <= TanhPoly::kMost ? x1 : map.cap2 * tanh_ex2(t1));
+      }
     }
   }
   if (kBias) {

@@ -86,3 +86,45 @@ def test_caps_to_the_end_of_their_range(dtype, shift, cap):
     """The reference that the weights are taken against must be that of the same scores: any other
     one is off by its error times the cap."""
     test_scores_keep_their_relative_precision(dtype, shift, cap)
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("cap", [50.0, 1e5])
+def test_a_row_at_the_cap_leaves_its_neighbours_alone(cap, slopes):
+    """One row in 32 has scores a thousand times the others': past the cap, where tanh takes
+    another form.  The other rows keep their precision."""
+    q, k, v = inputs(640, 2, 1, 0, 7)
+    q[::32] *= 1024.0
+    sl = torch.tensor([0.25, 0.0]) if slopes else None
+    at = torch.arange(640)
+    ref = R.attend(q, k, v, at, torch.zeros_like(at), at, SCALE, cap, sl)
+    _, top = causal(q, k, v, cap)
+    if slopes:  # the largest addend of a score that counts: the bias moves no score up
+        top = top + 0.25 * 640
+    out = fpx.span_path(*(x.bfloat16().cuda() for x in (q, k, v)), 128, softcap=cap,
+                        slopes=None if sl is None else sl.cuda(), softmax_scale=SCALE)
+    close(out["o"], out["lse"], ref, top, "bf16")
+
+
+@pytest.mark.parametrize("cap", [50.0, 1e5, 1e20])
+def test_decode_behind_a_shared_prompt(cap):
+    """The same two on the shared prompt's tensor-core path: 64 requests of 2 heads each, one request
+    in 16 with scores a thousand times the others'."""
+    S, n, page, hq = 64, 512, 128, 2
+    q, k, v = inputs(n, hq, 1, 0, 9)
+    q = q[:S].clone()
+    if cap < 1e20:
+        q[::16] *= 1024.0
+    table = torch.arange(n // page, dtype=torch.int32).repeat(S, 1).cuda()
+    ctx = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    kc, vc = (x.bfloat16().view(n // page, page, 1, 128).cuda() for x in (k, v))
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dp = fpx.decode_problem(q.bfloat16().cuda(), kc, ctx, table, softmax_scale=SCALE,
+                            group_ptr=dev([0, S]), prefix_pages=dev([n // page]))
+    ws = fpx.decode_workspace(dp)
+    o, lse = fpx.decode(dp, q.bfloat16().cuda(), kc, vc, ws, fpx.score_rule(cap))
+    assert fpx.status(ws) == 0
+    at, lo = torch.full((S,), n - 1), torch.zeros(S, dtype=torch.int64)
+    ref = R.attend(q, k, v, at, lo, at, SCALE, cap)
+    s = torch.einsum("nhd,ld->hnl", q, k[:, 0]) * SCALE
+    close(o, lse, ref, (cap * torch.tanh(s.abs() / cap)).amax(-1), "bf16")
