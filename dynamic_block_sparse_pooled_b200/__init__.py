@@ -403,13 +403,14 @@ def prefill(q, k, v, block: int, alpha: float, cu_seqlens=None, sink_blocks: int
             window_blocks: int = 1, softmax_scale: float = 0.0, q_scale=None, k_scale=None,
             v_scale=None, stream=None) -> dict:
     """The whole path on one stream: scores -> CSR -> O, LSE.  Raises on any recorded error."""
-    pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
-    ws = workspace(pf, -1, q.device)
-    scores = block_scores(pf, q, k, ws, stream=stream)
-    row_ptr, col_idx, nnz = select(pf, scores, alpha, ws, sink_blocks, window_blocks,
-                                   stream=stream)
-    o, lse = sparse_prefill(pf, q, k, v, row_ptr, col_idx, ws, stream=stream)
-    check(status(ws, stream), "device status")
+    with torch.cuda.stream(stream):  # the workspace's zeros and the outputs are that stream's too
+        pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
+        ws = workspace(pf, -1, q.device)
+        scores = block_scores(pf, q, k, ws, stream=stream)
+        row_ptr, col_idx, nnz = select(pf, scores, alpha, ws, sink_blocks, window_blocks,
+                                       stream=stream)
+        o, lse = sparse_prefill(pf, q, k, v, row_ptr, col_idx, ws, stream=stream)
+        check(status(ws, stream), "device status")
     return dict(problem=pf, scores=scores, row_ptr=row_ptr, col_idx=col_idx, nnz=nnz, o=o,
                 lse=lse)
 
@@ -482,12 +483,13 @@ def vs_path(q, k, v, block: int, n_probe: int, alpha_v: float, alpha_s: float, c
             stream=None) -> dict:
     """The query-probe path on one stream: probes -> vertical / slash bitmasks -> candidate
     blocks -> masked attention.  Raises on any recorded device-side error."""
-    pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
-    ws = vs_workspace(pf, n_probe, q.device)
-    vert, slash = probe_patterns(pf, q, k, n_probe, alpha_v, alpha_s, ws, stream=stream)
-    row_ptr, col_idx, nnz = vs_select(pf, vert, slash, ws, stream=stream)
-    o, lse = vs_prefill(pf, q, k, v, vert, slash, row_ptr, col_idx, ws, stream=stream)
-    check(status(ws, stream), "device status")
+    with torch.cuda.stream(stream):  # the workspace's zeros and the outputs are that stream's too
+        pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
+        ws = vs_workspace(pf, n_probe, q.device)
+        vert, slash = probe_patterns(pf, q, k, n_probe, alpha_v, alpha_s, ws, stream=stream)
+        row_ptr, col_idx, nnz = vs_select(pf, vert, slash, ws, stream=stream)
+        o, lse = vs_prefill(pf, q, k, v, vert, slash, row_ptr, col_idx, ws, stream=stream)
+        check(status(ws, stream), "device status")
     return dict(problem=pf, vert=vert, slash=slash, row_ptr=row_ptr, col_idx=col_idx, nnz=nnz,
                 o=o, lse=lse)
 
@@ -652,13 +654,14 @@ def span_path(q, k, v, block: int, cu_seqlens=None, doc_cu=None, prefix=None, so
     with torch.cuda.device(q.device):
         if stream is None:
             stream = torch.cuda.current_stream(q.device)
-        pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
-        ws = workspace(pf, -1, q.device)
-        lo, hi = spans(pf, doc_cu, prefix, device=q.device, stream=stream)
-        rule = score_rule(softcap, slopes, window, lo, hi)
-        row_ptr, col_idx, nnz = span_select(pf, rule, ws, stream=stream)
-        o, lse = span_prefill(pf, q, k, v, rule, row_ptr, col_idx, ws, stream=stream)
-        check(status(ws, stream), "device status")
+        with torch.cuda.stream(stream):  # the workspace's zeros and the offsets are that stream's too
+            pf = problem(q, k, block, cu_seqlens, softmax_scale, q_scale, k_scale, v_scale)
+            ws = workspace(pf, -1, q.device)
+            lo, hi = spans(pf, doc_cu, prefix, device=q.device, stream=stream)
+            rule = score_rule(softcap, slopes, window, lo, hi)
+            row_ptr, col_idx, nnz = span_select(pf, rule, ws, stream=stream)
+            o, lse = span_prefill(pf, q, k, v, rule, row_ptr, col_idx, ws, stream=stream)
+            check(status(ws, stream), "device status")
     return dict(problem=pf, rule=rule, row_ptr=row_ptr, col_idx=col_idx, nnz=nnz, o=o, lse=lse)
 
 

@@ -313,3 +313,26 @@ def test_default_capacity_and_another_stream():
     a, b = R.span_bounds([700], None, [700])
     R.check(o2, lse2, R.span_reference(q64, k64, v64, [700], a, b, 1 / math.sqrt(128)), "bf16",
             "bf16", 700, 128)
+
+
+def test_path_on_a_side_stream_while_the_current_one_is_busy():
+    """The whole path on another stream gives the same bits, with work queued on the current stream
+    that its own kernels do not wait for."""
+    lens = [700, 129]
+    (q, k, v), _, _ = make("bf16", lens, 4, 2, 128)
+    docs = torch.tensor([0, 300, 829], dtype=torch.int32, device="cuda")
+    want = fpx.span_path(q, k, v, 128, cumulative(lens), docs, None, 20.0, None, 200)
+    plain = fpx.prefill(q, k, v, 128, 0.3, cumulative(lens))
+    probe = fpx.vs_path(q, k, v, 128, 32, 1e-3, 1e-3, cumulative(lens))
+    busy = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(100):
+        busy = busy @ busy
+    got = fpx.span_path(q, k, v, 128, cumulative(lens), docs, None, 20.0, None, 200, stream=s)
+    got_plain = fpx.prefill(q, k, v, 128, 0.3, cumulative(lens), stream=s)
+    got_probe = fpx.vs_path(q, k, v, 128, 32, 1e-3, 1e-3, cumulative(lens), stream=s)
+    torch.cuda.synchronize()
+    for a, b in ((want, got), (plain, got_plain), (probe, got_probe)):
+        for name in ("o", "lse", "row_ptr", "nnz"):
+            assert torch.equal(a[name], b[name]), name

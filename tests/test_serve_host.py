@@ -249,3 +249,43 @@ def test_page_and_append_wrappers():
             fpx.kv_append(*args, ws)
     with pytest.raises(TypeError):
         fpx.kv_append(k, k, i32(4), c.half(), c, ws)
+
+
+# ---- the paths run on the caller's stream from their first byte on ----------------------------
+
+@pytest.mark.parametrize("path,args", [("prefill", (0.5,)), ("vs_path", (2, 0.5, 0.5)), ("span_path", ())])
+def test_paths_make_their_workspace_on_the_stream_they_launch_on(monkeypatch, path, args):
+    """The kernels write tables into the workspace: zeros that another stream still has to write
+    would land on top of them."""
+    inside = []
+
+    class Within:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            inside.append(self.what)
+
+        def __exit__(self, *_):
+            inside.pop()
+
+    class Reached(Exception):
+        pass
+
+    mine, seen = object(), []
+    monkeypatch.setattr(torch.cuda, "device", lambda d: Within("device"))
+    monkeypatch.setattr(torch.cuda, "stream", Within)
+    zeros = torch.zeros
+
+    def watched(*a, **kw):
+        seen.append(list(inside))
+        if kw.get("dtype") is torch.uint8:
+            raise Reached  # nothing is launched
+        return zeros(*a, **kw)
+
+    q = zeros(300, 2, 128, dtype=torch.bfloat16)
+    monkeypatch.setattr(torch, "zeros", watched)
+    with pytest.raises(Reached):
+        getattr(fpx, path)(q, q, q, 128, *args, stream=mine)
+    assert seen and all(mine in s for s in seen)
+    assert not inside
