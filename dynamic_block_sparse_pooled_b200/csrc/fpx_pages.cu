@@ -13,17 +13,21 @@ namespace pages {
 
 constexpr int kThreads = 1024;
 // Tokens up to which the planning CTA moves the pages and writes the slot map itself; above, a second
-// launch does both with the whole GPU.  Replayed from a graph, 256 / 2048 / 4096 / 8192 / 16384 tokens:
-// 4.2 / 6.2 / 8.2 / 12.3 / 18.6 us in one launch, 6.2 / 8.2 / 8.2 / 8.3 / 9.5 in two.
+// launch does both with the whole GPU.  Replayed from a graph, prompts of 256 tokens on pages of 16, 256 /
+// 2048 / 4096 / 8192 / 16384 tokens in all: 3.3 / 4.3 / 5.7 / 8.6 / 15.0 us in one launch, 4.9 / 5.1 / 5.5
+// / 5.7 / 6.1 in two.  Pages given back are work too, but the host does not know how many they are, and
+// a step in which many come is rare: one request of 8192 pages 8.2 us in one launch and 7.0 in two, 64
+// requests of 512 pages 21 and 10, 1024 requests of 188 pages 161 and 52.
 constexpr int kInlineTokens = 4096;
 
-// What the planning CTA leaves for the second launch: pages given and taken before each request, and
-// in [num_seqs] their totals.
+// Pages given and taken before each request; for the second launch in [num_seqs] their totals.
 struct Plan {
   int32_t* give;
   int32_t* take;
-  int32_t* ok;  // 1 where the call goes through
+  int32_t* ok;  // second launch: 1 where the call goes through, then the stack's height
 };
+
+constexpr int kPushes = 4;  // pages that a thread gives back at a time: their loads overlap
 
 struct ResizeArgs {
   int num_seqs, page, log2_page, num_pages, pages_per_seq, token_capacity;
@@ -97,10 +101,61 @@ __device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
           __shfl_up_sync(0xffffffffu, x.tokens, o)};
 }
 
+// The i-th page given back by this call.
+__device__ __forceinline__ int given_at(const ResizeArgs& a, const Plan& plan, int i) {
+  const int s = owner_of(plan.give, a.num_seqs, i);
+  const int first = max(pages_of(a, a.new_lens[s]), a.keep ? a.keep[s] : 0);
+  return a.table[static_cast<int64_t>(s) * a.pages_per_seq + first + i - plan.give[s]];
+}
+// The page at place x of the stack after the pushes.  A page pushed by this call is looked up where
+// it comes from, so that no thread waits for another one's push.
+__device__ __forceinline__ int stack_at(const ResizeArgs& a, const Plan& plan, int count, int x) {
+  return x < count ? a.free_pages[x] : given_at(a, plan, x - count);
+}
+
+// Pushes, pops and the slot map, an item each for the threads first, first + step, .. (a request gives
+// or takes, so no row of the table is both read here and written; pushes go above the height that
+// pops read below).
+__device__ __forceinline__ void make_moves(const ResizeArgs& a, const Plan& plan, int count,
+                                           int gives, int takes, int total, int first, int step,
+                                           StatusBlock* st) {
+  const int top = count + gives;
+  if (first == 0) *a.free_count_out = top - takes;
+  for (int i0 = first; i0 < gives; i0 += kPushes * step) {
+    int pg[kPushes];
+#pragma unroll
+    for (int b = 0; b < kPushes; ++b)
+      if (i0 + b * step < gives) pg[b] = given_at(a, plan, i0 + b * step);
+#pragma unroll
+    for (int b = 0; b < kPushes; ++b)
+      if (i0 + b * step < gives) a.free_pages[count + i0 + b * step] = pg[b];
+  }
+  for (int i = first; i < takes; i += step) {
+    const int s = owner_of(plan.take, a.num_seqs, i);
+    const int pg = stack_at(a, plan, count, top - 1 - i);
+    if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
+    a.table[static_cast<int64_t>(s) * a.pages_per_seq + pages_of(a, a.lens[s]) + i - plan.take[s]] = pg;
+  }
+  for (int t = first; t < a.token_capacity; t += step) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int s = owner_of(a.cu_new, a.num_seqs, t);
+      const int len = a.lens[s], have = pages_of(a, len);
+      pos = len + t - a.cu_new[s];
+      const int j = pos >> a.log2_page;
+      const int pg = j < have ? a.table[static_cast<int64_t>(s) * a.pages_per_seq + j]
+                              : stack_at(a, plan, count, top - 1 - (plan.take[s] + j - have));
+      slot = slot_at(a, pg, s, pos, st);
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+}
+
 // One CTA: thread t owns a run of consecutive requests.  Pass 1 sums what they give, take and add;
 // a scan over the threads gives each its first place on the stack and among the tokens; the
-// totals are checked before anything is written.  Then, for few tokens, cu_new and the pushes, the
-// pops after all pushes, and the slot map; else cu_new and the plan of the second launch.
+// totals are checked before anything is written.  Then cu_new and the plan, and from it the moves,
+// spread over this CTA's threads for few tokens, else over the second launch's.
 // (The stack needs the requests' order, so the scan is the operator; it is latency-bound: two
 // reads of the lengths and the scan.)
 template <bool kInline>
@@ -157,108 +212,37 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(ResizeArgs a, Plan pla
       for (int t = tid; t < a.token_capacity; t += kThreads) a.slots[t] = a.positions[t] = -1;
     return;
   }
-  const int top = count + static_cast<int>(all.give);
+  const int gives = static_cast<int>(all.give), takes = static_cast<int>(all.take);
   const int total = static_cast<int>(all.tokens);
-  int give = static_cast<int>(at.give), take = static_cast<int>(at.take);
-  int tok = static_cast<int>(at.tokens);
   for (int s = s0; s < s1; ++s) {
     change_of(a, s, c);
-    a.cu_new[s] = tok;
-    tok += c.tokens;
-    if (kInline) {
-      const int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.first_give;
-      for (int i = 0; i < c.give; ++i) a.free_pages[count + give++] = row[i];
-    } else {
-      plan.give[s] = give;
-      plan.take[s] = take;
-      give += c.give;
-      take += c.take;
-    }
+    a.cu_new[s] = static_cast<int>(at.tokens);
+    plan.give[s] = static_cast<int>(at.give);
+    plan.take[s] = static_cast<int>(at.take);
+    at = at + Sums{c.give, c.take, c.tokens};
   }
   if (tid == 0) {
     a.cu_new[a.num_seqs] = total;
-    // a second launch reads the height as it was: it writes the new one (see moves_kernel)
-    if (kInline) *a.free_count_out = top - static_cast<int>(all.take);
     if (!kInline) {
-      plan.give[a.num_seqs] = static_cast<int>(all.give);
-      plan.take[a.num_seqs] = static_cast<int>(all.take);
+      plan.give[a.num_seqs] = gives;
+      plan.take[a.num_seqs] = takes;
       plan.ok[0] = 1;
-      plan.ok[1] = count;
+      plan.ok[1] = count;  // the second launch writes the new height, which may lie over it
     }
   }
   if (!kInline) return;
-  __syncthreads();  // every push is on the stack, cu_new is written
-  for (int s = s0; s < s1; ++s) {
-    change_of(a, s, c);
-    int32_t* row = a.table + static_cast<int64_t>(s) * a.pages_per_seq + c.have;
-    for (int i = 0; i < c.take; ++i) {
-      const int pg = a.free_pages[top - 1 - take++];
-      if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
-      row[i] = pg;
-    }
-  }
-  __syncthreads();  // the table is written
-  for (int t = tid; t < a.token_capacity; t += kThreads) {
-    int slot = -1, pos = -1;
-    if (t < total) {
-      const int s = owner_of(a.cu_new, a.num_seqs, t);
-      pos = a.lens[s] + t - a.cu_new[s];
-      slot = slot_at(a, a.table[static_cast<int64_t>(s) * a.pages_per_seq + (pos >> a.log2_page)],
-                     s, pos, st);
-    }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
-  }
+  __syncthreads();  // cu_new and the plan are written
+  make_moves(a, plan, count, gives, takes, total, tid, kThreads, st);
 }
 
-// The page at place x of the stack after the pushes.  A page pushed by this call is looked up where
-// it comes from, so that no thread waits for another one's push.
-__device__ __forceinline__ int stack_at(const ResizeArgs& a, const Plan& plan, int count, int x) {
-  if (x < count) return a.free_pages[x];
-  const int i = x - count, s = owner_of(plan.give, a.num_seqs, i);
-  Change c;
-  change_of(a, s, c);
-  return a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.first_give + i - plan.give[s]];
-}
-
-// Pushes, pops and the slot map, a thread each (a request gives or takes, so no row of the table is
-// both read here and written; pushes go above the height that pops read below).
 __global__ void __launch_bounds__(256) moves_kernel(ResizeArgs a, Plan plan, StatusBlock* st) {
   pdl_enter();  // after the previous kernel on the stream
   const int first = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
-  const bool ok = plan.ok[0] != 0;
-  const int count = plan.ok[1];
-  const int gives = ok ? plan.give[a.num_seqs] : 0, takes = ok ? plan.take[a.num_seqs] : 0;
-  const int total = a.cu_new[a.num_seqs];  // 0 where the call is refused
-  const int top = count + gives;
-  Change c;
-  if (ok && first == 0) *a.free_count_out = top - takes;
-  for (int i = first; i < gives; i += step) {
-    const int s = owner_of(plan.give, a.num_seqs, i);
-    change_of(a, s, c);
-    a.free_pages[count + i] =
-        a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.first_give + i - plan.give[s]];
-  }
-  for (int i = first; i < takes; i += step) {
-    const int s = owner_of(plan.take, a.num_seqs, i);
-    change_of(a, s, c);
-    const int pg = stack_at(a, plan, count, top - 1 - i);
-    if (pg < 0 || pg >= a.num_pages) record_error(st, FPX_ERR_DEVICE_INPUT, 53, s, pg);
-    a.table[static_cast<int64_t>(s) * a.pages_per_seq + c.have + i - plan.take[s]] = pg;
-  }
-  for (int t = first; t < a.token_capacity; t += step) {
-    int slot = -1, pos = -1;
-    if (t < total) {
-      const int s = owner_of(a.cu_new, a.num_seqs, t);
-      change_of(a, s, c);
-      pos = a.lens[s] + t - a.cu_new[s];
-      const int j = pos >> a.log2_page;
-      const int pg = j < c.have ? a.table[static_cast<int64_t>(s) * a.pages_per_seq + j]
-                                : stack_at(a, plan, count, top - 1 - (plan.take[s] + j - c.have));
-      slot = slot_at(a, pg, s, pos, st);
-    }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+  if (plan.ok[0] != 0) {
+    make_moves(a, plan, plan.ok[1], plan.give[a.num_seqs], plan.take[a.num_seqs],
+               a.cu_new[a.num_seqs], first, step, st);
+  } else {
+    for (int t = first; t < a.token_capacity; t += step) a.slots[t] = a.positions[t] = -1;
   }
 }
 

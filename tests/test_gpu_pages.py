@@ -268,3 +268,46 @@ def test_serving_steps(dtype, captured):
                            1 / math.sqrt(d), cap_, slopes)
             R.check(o[s:s + 1], lse[:, s:s + 1], ref, "f16" if e4m3 else "bf16", "bf16", n, d)
     assert int(count) == num - 3 - 1  # request 0 holds three pages, entry 2 one
+
+
+@pytest.mark.parametrize("cap", [8, 6000])
+@pytest.mark.parametrize("shape", ["release", "grow", "both"])
+def test_one_request_moves_thousands_of_pages(cap, shape):
+    """A 131072-token request with pages of 16 ends in a call that adds few tokens, one of 4000 begins,
+    or both; the others step by a token."""
+    page, width = 16, 8192
+    lens, new = [3, 40, 0, 15, 16], [4, 41, 0, 16, 17]
+    if shape != "grow":
+        lens[0], new[0] = 131072, 0
+    if shape != "release":
+        lens[2], new[2] = 1, 4000 if cap > 8 else 3
+    rng = random.Random(5)
+    table, free, count, pages = state(rng, lens, page, width, 300)
+    code, got = resize(lens, new, table, free, count, page, pages, cap)
+    assert code == 0
+    assert got == R.page_reference(lens, new, table, free, count, page, pages, cap)
+
+
+def test_time_does_not_follow_the_longest_request():
+    """8192 pages given back by one request take no longer than by 1024 requests, 8 each, within a
+    factor (the threads share the pages, not the requests; a walk by one thread is some 50 times)."""
+    page, best = 16, {}
+    for num, each in ((1024, 8), (1, 8192)):
+        lens, new = dev([each * page] * num), dev([0] * num)
+        table = torch.arange(num * each, dtype=torch.int32, device="cuda").view(num, each)
+        free, count = torch.zeros(num * each, dtype=torch.int32, device="cuda"), dev([0])
+        out, ws = dev([0]), fpx.page_workspace(num)
+        bufs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (num + 1, 1, 1)]
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(20):
+                fpx.page_resize(lens, new, table, free, count, page, num * each, 1, ws, count_out=out,
+                                cu_new=bufs[0], slots=bufs[1], positions=bufs[2])
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        best[num] = min(times)
+        assert fpx.status(ws) == 0 and int(out) == num * each and torch.equal(free, table.flatten())
+    assert best[1] <= 4 * best[1024], best
