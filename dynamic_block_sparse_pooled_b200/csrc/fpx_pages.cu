@@ -127,8 +127,12 @@ __device__ __forceinline__ void make_moves(const ResizeArgs& a, const Plan& plan
     for (int b = 0; b < kPushes; ++b)
       if (i0 + b * step < gives) pg[b] = given_at(a, plan, i0 + b * step);
 #pragma unroll
-    for (int b = 0; b < kPushes; ++b)
-      if (i0 + b * step < gives) a.free_pages[count + i0 + b * step] = pg[b];
+    for (int b = 0; b < kPushes; ++b) {
+      if (i0 + b * step >= gives) continue;
+      if (pg[b] < 0 || pg[b] >= a.num_pages)
+        record_error(st, FPX_ERR_DEVICE_INPUT, 55, i0 + b * step, pg[b]);
+      a.free_pages[count + i0 + b * step] = pg[b];
+    }
   }
   for (int i = first; i < takes; i += step) {
     const int s = owner_of(plan.take, a.num_seqs, i);

@@ -355,7 +355,8 @@ fpx_status fpx_span_prefill(const fpx_problem* p, const void* q, const void* k, 
  * FPX_ERR_DEVICE_INPUT; too few free pages, a stack that would pass num_pages, or more tokens than
  * token_capacity: FPX_ERR_CAPACITY.  Then nothing changes: the table and the stack keep their
  * values, the count is copied, cu_new is all zero and slots and positions all -1.  A page id
- * outside [0, num_pages), of the stack or the table, gives slot -1 and FPX_ERR_DEVICE_INPUT.
+ * outside [0, num_pages), of the stack or the table, gives slot -1 and FPX_ERR_DEVICE_INPUT; one that
+ * is given back is recorded too, and lies on the stack.
  *   ws  device workspace >= fpx_page_workspace_bytes(num_seqs); calls that may overlap need one each.
  *       fpx_kv_append takes one of any size (it only records errors there).
  */

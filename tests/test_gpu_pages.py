@@ -311,3 +311,12 @@ def test_time_does_not_follow_the_longest_request():
         best[num] = min(times)
         assert fpx.status(ws) == 0 and int(out) == num * each and torch.equal(free, table.flatten())
     assert best[1] <= 4 * best[1024], best
+
+
+@pytest.mark.parametrize("cap", [4, 6000])
+@pytest.mark.parametrize("bad", [-1, 6, 2 ** 30])
+def test_a_bad_page_given_back_is_recorded(cap, bad):
+    code, got = resize([40, 5], [10, 6], [[5, bad, 3], [0, -1, -1]], [4, -7, -7, -7, -7, -7], 1, 16, 6,
+                       cap)
+    assert code == -7
+    assert got["free"][:3] == [4, bad, 3] and got["count"] == 3 and got["slots"][:2] == [5, -1]
