@@ -27,6 +27,9 @@ struct Plan {
   int32_t* ok;  // second launch: 1 where the call goes through, then the stack's height
 };
 
+// Requests and tokens of a call: a thread's next index, one stride of the largest grid (303104) or one
+// CTA's round of requests further, has to stay within 32 bits.
+constexpr int kMostItems = INT32_MAX - (1 << 20);
 constexpr int kPushes = 4;  // pages that a thread gives back at a time: their loads overlap
 
 struct ResizeArgs {
@@ -355,7 +358,9 @@ cudaError_t launch_resize(const ResizeArgs& a, void* ws, cudaStream_t s) {
   }
   FPX_CHAIN((resize_kernel<false>), 1, kThreads, 0, s, a, plan, st);
   const int want = (a.token_capacity - 1) / 256 + 1;
-  FPX_CHAIN(moves_kernel, want < 148 * 8 ? want : 148 * 8, 256, 0, s, a, plan, st);
+  constexpr int kMoveCtas = 148 * 8;
+  static_assert(kMoveCtas * 256 <= (1 << 20), "kMostItems");
+  FPX_CHAIN(moves_kernel, want < kMoveCtas ? want : kMoveCtas, 256, 0, s, a, plan, st);
   return cudaGetLastError();
 }
 
@@ -399,7 +404,8 @@ fpx_status fpx_page_resize(int32_t num_seqs, int32_t page, int32_t num_pages,
   if (page < 16 || page > 128 || (page & (page - 1)) != 0) return FPX_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_pages) * page > INT32_MAX ||
       static_cast<int64_t>(pages_per_seq) * page > INT32_MAX - page ||
-      static_cast<int64_t>(pages_per_seq) * num_seqs > INT32_MAX)
+      static_cast<int64_t>(pages_per_seq) * num_seqs > INT32_MAX ||
+      num_seqs > pages::kMostItems || token_capacity > pages::kMostItems)
     return FPX_ERR_UNSUPPORTED;
   if (!lens_d || !new_lens_d || !block_table_d || !free_pages_d || !free_count_d ||
       !free_count_out_d || !cu_new_d || !ws)

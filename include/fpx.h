@@ -349,6 +349,7 @@ fpx_status fpx_span_prefill(const fpx_problem* p, const void* q, const void* k, 
  *   slots_d, positions_d  device int32 [token_capacity]: for token t of request s (the t-th added),
  *                       at cu_new[s] + t: its cache row page_id * page + offset, and its position
  *                       lens[s] + t.  Entries from cu_new[num_seqs] on are set to -1.
+ * num_seqs and token_capacity are at most 2^31 - 2^20 - 1 (FPX_ERR_UNSUPPORTED beyond).
  * lens, new_lens and the free count are only read (but where free_count_out_d is free_count_d):
  * a call repeated on the same inputs gives the same outputs.
  * Device-side conditions: a length that is negative or beyond the table, or keep_pages < 0:

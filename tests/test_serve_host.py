@@ -289,3 +289,16 @@ def test_paths_make_their_workspace_on_the_stream_they_launch_on(monkeypatch, pa
         getattr(fpx, path)(q, q, q, 128, *args, stream=mine)
     assert seen and all(mine in s for s in seen)
     assert not inside
+
+
+@pytest.mark.parametrize("i", [0, 14])
+def test_page_counts_whose_strides_would_pass_32_bits(i):
+    """Requests or tokens so near 2^31 that a thread's next index would wrap to a negative one and be
+    read or written in front of the buffers.  Just below, the next check answers (a workspace that is
+    too small): nothing is launched."""
+    lib = fpx.load()
+    most = 2 ** 31 - 2 ** 20 - 1
+    full = [4, 16, 64, A, A, None, A, 1, A, A, A, A, A, A, 100, A, 0, None]
+    for n, want in ((most + 1, -2), (2 ** 31 - 1, -2), (most, -4)):
+        full[i] = n
+        assert lib.fpx_page_resize(*full) == want, n
