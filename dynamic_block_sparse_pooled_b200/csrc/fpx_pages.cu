@@ -456,8 +456,8 @@ fpx_status fpx_kv_append(fpx_dtype dtype, int32_t hkv, int32_t d, int32_t num_to
   if (!ws || (num_tokens > 0 && (!k || !v || !slots_d || !k_cache || !v_cache)))
     return FPX_ERR_INVALID_ARG;
   const int64_t es = dtype == FPX_F32 ? 4 : 2;
-  if (k_stride < row || v_stride < row || k_stride > INT64_MAX / 4 / (num_tokens + 1) ||
-      v_stride > INT64_MAX / 4 / (num_tokens + 1))
+  const int64_t most = INT64_MAX / 4 / (static_cast<int64_t>(num_tokens) + 1);  // bytes fit int64
+  if (k_stride < row || v_stride < row || k_stride > most || v_stride > most)
     return FPX_ERR_INVALID_ARG;
   if (!is_aligned(k, 16) || !is_aligned(v, 16) || (k_stride * es) % 16 != 0 ||
       (v_stride * es) % 16 != 0 || !is_aligned(slots_d, 4) || !is_aligned(k_cache, 16) ||

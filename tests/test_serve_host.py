@@ -302,3 +302,14 @@ def test_page_counts_whose_strides_would_pass_32_bits(i):
     for n, want in ((most + 1, -2), (2 ** 31 - 1, -2), (most, -4)):
         full[i] = n
         assert lib.fpx_page_resize(*full) == want, n
+
+
+def test_append_of_the_most_tokens_is_checked_like_any_other():
+    """2^31 - 1 tokens: their number plus one does not fit 32 bits.  The workspace is too small, which
+    is the last check: nothing is launched."""
+    lib = fpx.load()
+    row = 2 * 128
+    args = [fpx.BF16, 2, 128, 2 ** 31 - 1, A, row, A, row, A, A, A, 160, None, None, A, 8, None]
+    assert lib.fpx_kv_append(*args) == -4
+    args[5] = 2 ** 60
+    assert lib.fpx_kv_append(*args) == -1
