@@ -516,7 +516,10 @@ def _expect(name: str, t: Optional[torch.Tensor], dtype, device: int = -2, numel
 
 def _call(name: str, device: int, stream, *args) -> None:
     """Calls entry point `name` with the stream as its last argument (default: the device's current
-    one) and the device current."""
+    one) and the device current.  Host tensors (device -1) are refused: a kernel would read their
+    addresses."""
+    if device < 0:
+        raise ValueError(f"{name}: tensors must be on a GPU")
     fn = getattr(_lib or load(), name)
     handle = stream.cuda_stream if stream is not None else \
         torch._C._cuda_getCurrentRawStream(device)
@@ -568,6 +571,8 @@ def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
     tokens.  `device` is needed only where no tensor names one."""
     given = [t for t in (key_lo, key_hi, doc_cu, prefix, pf.cu_d) if t is not None]
     on = given[0].device if given else torch.device(device or "cuda")
+    if on.type != "cuda":
+        raise ValueError("fpx_spans: tensors must be on a GPU")
     dev = on.index if on.index is not None else torch.cuda.current_device()
     total = pf.struct.total_tokens
     docs = 0 if doc_cu is None else doc_cu.numel() - 1

@@ -313,3 +313,21 @@ def test_append_of_the_most_tokens_is_checked_like_any_other():
     assert lib.fpx_kv_append(*args) == -4
     args[5] = 2 ** 60
     assert lib.fpx_kv_append(*args) == -1
+
+
+def test_host_tensors_are_refused():
+    """Calls that are right but for lying in host memory: their addresses never reach a kernel."""
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    q, c = torch.zeros(3, 4, 128, dtype=torch.bfloat16), torch.zeros(2, 128, 4, 128, dtype=torch.bfloat16)
+    pf = fpx.problem(q, q, 128)
+    lo, hi = i32(3), i32(3)
+    r = fpx.score_rule(key_lo=lo, key_hi=hi)
+    dp = fpx.decode_problem(q, c, i32(3), i32(3, 1))
+    calls = [lambda: fpx.spans(pf, None, i32(1), lo, hi), lambda: fpx.span_select(pf, r, ws),
+             lambda: fpx.span_prefill(pf, q, q, q, r, i32(5), i32(4), ws),
+             lambda: fpx.decode(dp, q, c, c, ws),
+             lambda: fpx.page_resize(i32(2), i32(2), i32(2, 2), i32(4), i32(1), 16, 4, 8, ws),
+             lambda: fpx.kv_append(q, q, i32(3), c, c, ws)]
+    for call in calls:
+        with pytest.raises(ValueError, match="must be on a GPU"):
+            call()
