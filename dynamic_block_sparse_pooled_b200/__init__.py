@@ -563,6 +563,15 @@ def _check_rule(rule: ScoreRule, hq: int, tokens: int, device: int) -> None:
     _expect("key_hi", hi, torch.int32, device, tokens)
 
 
+def _check_problem(pf: Prefill, device: int) -> None:
+    """The problem's own tensors (offsets, e4m3 scales) must lie where the call's do."""
+    _expect("cu_seqlens", pf.cu_d, torch.int32, device)
+    if pf.struct.dtype == E4M3:
+        for name, t in zip(("q_scale", "k_scale", "v_scale"), pf.scales):
+            heads = pf.struct.hq if name == "q_scale" else pf.struct.hkv
+            _expect(name, t, torch.float32, device, heads)
+
+
 def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
           prefix: Optional[torch.Tensor] = None, key_lo: Optional[torch.Tensor] = None,
           key_hi: Optional[torch.Tensor] = None, device=None, stream=None):
@@ -578,6 +587,7 @@ def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
     docs = 0 if doc_cu is None else doc_cu.numel() - 1
     if doc_cu is not None and docs < 1:
         raise ValueError("doc_cu needs at least one document")
+    _check_problem(pf, dev)
     _expect("doc_cu", doc_cu, torch.int32, dev)
     _expect("prefix", prefix, torch.int32, dev, docs if doc_cu is not None else pf.struct.num_seqs)
     key_lo = _empty(total, torch.int32, on, stream) if key_lo is None else key_lo
@@ -602,6 +612,7 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
     """fpx_span_select -> (row_ptr, col_idx, nnz): the key blocks that the rule's spans reach."""
     dev, index = ws.device, ws.get_device()
     _expect("ws", ws, torch.uint8, index)
+    _check_problem(pf, index)
     _check_rule(rule, pf.struct.hq, pf.struct.total_tokens, index)
     if row_ptr is None:
         row_ptr = _empty(pf.rows + 1, torch.int32, dev, stream)
@@ -615,6 +626,8 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
     if nnz is None:
         nnz = _empty(1, torch.int64, dev, stream)
     _check_csr_outputs(pf, row_ptr, col_idx, nnz, cap)
+    for name, t in (("row_ptr", row_ptr), ("col_idx", col_idx), ("nnz", nnz)):
+        _expect(name, t, t.dtype, index)
     _call("fpx_span_select", index, stream, pf.ptr, ctypes.byref(rule), _ptr(row_ptr),
           _ptr(col_idx), cap, _ptr(nnz), _ptr(ws), ws.numel())
     return row_ptr, col_idx, nnz
@@ -635,6 +648,9 @@ def span_prefill(pf: Prefill, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             raise ValueError(f"{name} must hold {rows} rows of [{p.hkv}, {p.d}]")
     if _DTYPES[q.dtype] != p.dtype:
         raise TypeError(f"q is {q.dtype}, the problem was described with another type")
+    _check_problem(pf, dev)
+    if kv is not None:
+        _expect("block_table", getattr(kv, "_keep", None), torch.int32, dev)
     _check_rule(rule, p.hq, p.total_tokens, dev)
     _expect("row_ptr", row_ptr, torch.int32, dev, pf.rows + 1)
     _expect("col_idx", col_idx, torch.int32, dev)

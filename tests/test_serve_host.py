@@ -331,3 +331,43 @@ def test_host_tensors_are_refused():
     for call in calls:
         with pytest.raises(ValueError, match="must be on a GPU"):
             call()
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lies on GPU 1."""
+
+    def get_device(self):
+        return 1
+
+
+def test_a_problem_on_another_device_is_refused():
+    """Offsets, scales, tables and outputs that lie on another device than the call's tensors."""
+    away = lambda t: t.as_subclass(Elsewhere)  # noqa: E731
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    pf = fpx.problem(q, q, 128, [0, 3])
+    pf.cu_d = away(pf.cu_d)
+    lo, hi, r = i32(3), i32(3), fpx.score_rule()
+    for call in (lambda: fpx.span_select(pf, r, ws),
+                 lambda: fpx.span_prefill(pf, q, q, q, r, i32(5), i32(4), ws)):
+        with pytest.raises(ValueError, match="cu_seqlens is on"):
+            call()
+    e = q.to(torch.float8_e4m3fn)
+    one = torch.ones(4)
+    pf = fpx.problem(e, e, 128, None, 0.0, one, away(one), one)
+    with pytest.raises(ValueError, match="k_scale is on"):
+        fpx.span_prefill(pf, e, e, e, r, i32(5), i32(4), ws)
+    pf = fpx.problem(e, e, 128, None, 0.0, one, one, torch.ones(3))
+    with pytest.raises(ValueError, match="v_scale holds 3"):
+        fpx.span_prefill(pf, e, e, e, r, i32(5), i32(4), ws)
+    pf = fpx.problem(q, q, 128)
+    kv = fpx.paged_kv(away(i32(1, 1)), 1)
+    c = torch.zeros(1, 128, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="block_table is on"):
+        fpx.span_prefill(pf, q, c, c, r, i32(5), i32(4), ws, kv=kv)
+    away_csr = (away(i32(5)), away(i32(64)), away(torch.zeros(1, dtype=torch.int64)))
+    for k in range(3):
+        csr = [i32(5), i32(64), torch.zeros(1, dtype=torch.int64)]
+        csr[k] = away_csr[k]
+        with pytest.raises(ValueError, match="is on"):
+            fpx.span_select(pf, r, ws, *csr)
