@@ -600,11 +600,12 @@ def spans(pf: Prefill, doc_cu: Optional[torch.Tensor] = None,
 
 
 def span_capacity(pf: Prefill) -> int:
-    """CSR entries that a rule can need at most: Hq * sum of (blocks of a sequence)^2."""
+    """CSR entries that a rule can need at most: Hq * sum of (blocks of a sequence)^2, or as many as
+    a call takes, 2^31 - 1.  (Selections that pass it are recorded as any that pass their capacity.)"""
     b = pf.struct.block
     lens = np.diff(pf.cu_h.astype(np.int64)) if pf.cu_h is not None else \
         np.array([pf.struct.total_tokens], dtype=np.int64)
-    return int(pf.struct.hq * ((-(-lens // b)) ** 2).sum())
+    return min(int(pf.struct.hq * ((-(-lens // b)) ** 2).sum()), 2 ** 31 - 1)
 
 
 def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, col_idx=None,

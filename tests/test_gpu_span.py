@@ -336,3 +336,21 @@ def test_path_on_a_side_stream_while_the_current_one_is_busy():
     for a, b in ((want, got), (plain, got_plain), (probe, got_probe)):
         for name in ("o", "lse", "row_ptr", "nnz"):
             assert torch.equal(a[name], b[name]), name
+
+
+def test_default_list_of_a_million_tokens():
+    """32 heads of 8192 blocks under key spans and a window: the default list takes every block that
+    the window reaches (33 of a row, fewer at its start)."""
+    t, hq, b = 2 ** 20, 32, 128
+    q = torch.empty(1, hq, 128, dtype=torch.bfloat16, device="cuda").expand(t, hq, 128)
+    pf = fpx.problem(q, q[:, :8], b)
+    ws = fpx.workspace(pf, 1)
+    lo, hi = fpx.spans(pf, device="cuda")
+    rp, ci, nnz = fpx.span_select(pf, fpx.score_rule(window=32 * b, key_lo=lo, key_hi=hi), ws)
+    assert fpx.status(ws) == 0
+    n = t // b
+    want = torch.clamp(torch.arange(1, n + 1, device="cuda"), max=33)
+    assert torch.equal((rp[1:] - rp[:-1]).view(hq, n).long(), want.expand(hq, n))
+    assert int(nnz) == hq * int(want.sum()) == int(rp[-1])
+    last = ci[int(nnz) - 33:int(nnz)]
+    assert torch.equal(last.long(), torch.arange(n - 33, n, device="cuda"))

@@ -371,3 +371,18 @@ def test_a_problem_on_another_device_is_refused():
         csr[k] = away_csr[k]
         with pytest.raises(ValueError, match="is on"):
             fpx.span_select(pf, r, ws, *csr)
+
+
+def test_default_list_of_a_long_layer_is_one_that_the_call_takes():
+    """A million tokens, 32 heads: 2^31 entries would hold every block, one more than a call takes; a
+    window needs a few million of them."""
+    class Layer:
+        struct, cu_h = fpx.Problem(), None
+    Layer.struct.total_tokens, Layer.struct.hq, Layer.struct.block = 2 ** 20, 32, 128
+    assert fpx.span_capacity(Layer) == 2 ** 31 - 1
+    lib, p = fpx.load(), problem(seqlens=(2 ** 20,), hq=32, hkv=8)
+    # the capacity is taken: what the call refuses is nnz, misaligned
+    for cap, want in ((2 ** 31, -1), (2 ** 31 - 1, -3)):
+        assert lib.fpx_span_select(ctypes.byref(p), rule(), A, A, cap, A + 4, A, 2 ** 50, None) == want
+    Layer.struct.total_tokens, Layer.struct.hq = 700, 2
+    assert fpx.span_capacity(Layer) == 2 * 36
