@@ -45,6 +45,7 @@ KERNELS_PER_STEP = 10  # plan+pool+score, plan+count+scan+emit, plan+order+atten
 ATTN_SOURCES = ("dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cu",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_softmax.cuh",
+                "dynamic_block_sparse_pooled_b200/csrc/fpx_rule.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_sm100.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_common.cuh")
 ATTN_TRAFFIC_DIGEST = "a3978d45273cf2bed10370f18451224d9ea417207bc35772aac5243e97c895d5"

@@ -126,3 +126,21 @@ def test_selection_stats_match_the_oracle(alpha, sink, window):
                 loads += int(u.sum())
     assert st["kv_tile_loads"] == loads
     assert st["union_excess_tiles"] == 0
+
+
+def test_digest_covers_every_header_of_the_attention_kernel():
+    """Whatever the kernel's source includes, from header to header, is in the digest; left out are
+    fpx_internal.h (launches and declarations, no kernel code; its own includes count) and the public
+    header."""
+    import re
+    csrc = os.path.join(bench.ROOT, "dynamic_block_sparse_pooled_b200", "csrc")
+    todo, seen = ["fpx_attn_sm100.cu"], set()
+    while todo:
+        name = todo.pop()
+        if name in seen or not os.path.exists(os.path.join(csrc, name)):
+            continue
+        seen.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            todo += re.findall(r'#include "([^"]+)"', f.read())
+    seen = {n for n in seen if not n.startswith("..")} - {"fpx_internal.h"}
+    assert seen == {os.path.basename(p) for p in bench.ATTN_SOURCES}
