@@ -565,7 +565,8 @@ def _check_rule(rule: ScoreRule, hq: int, tokens: int, device: int) -> None:
 
 def _check_problem(pf: Prefill, device: int) -> None:
     """The problem's own tensors (offsets, e4m3 scales) must lie where the call's do."""
-    _expect("cu_seqlens", pf.cu_d, torch.int32, device)
+    if pf.cu_d is not None and pf.cu_d.get_device() != device:
+        _expect("cu_seqlens", pf.cu_d, torch.int32, device)
     if pf.struct.dtype == E4M3:
         for name, t in zip(("q_scale", "k_scale", "v_scale"), pf.scales):
             heads = pf.struct.hq if name == "q_scale" else pf.struct.hkv
@@ -627,8 +628,9 @@ def span_select(pf: Prefill, rule: ScoreRule, ws: torch.Tensor, row_ptr=None, co
     if nnz is None:
         nnz = _empty(1, torch.int64, dev, stream)
     _check_csr_outputs(pf, row_ptr, col_idx, nnz, cap)
-    for name, t in (("row_ptr", row_ptr), ("col_idx", col_idx), ("nnz", nnz)):
-        _expect(name, t, t.dtype, index)
+    if not row_ptr.get_device() == col_idx.get_device() == nnz.get_device() == index:
+        raise ValueError(f"row_ptr is on {row_ptr.device}, col_idx is on {col_idx.device} and nnz "
+                         f"is on {nnz.device}, expected device {index}")
     _call("fpx_span_select", index, stream, pf.ptr, ctypes.byref(rule), _ptr(row_ptr),
           _ptr(col_idx), cap, _ptr(nnz), _ptr(ws), ws.numel())
     return row_ptr, col_idx, nnz

@@ -211,7 +211,9 @@ __device__ __forceinline__ void bits128(const uint32_t* __restrict__ row, int wo
 // without a cap or a bias does not carry their code through the row loop: bit 0 a rule, bit 1 a
 // cap, bit 2 a distance bias.  (8192 tokens, 32 heads: no rule 467 us, cap 640; 13875 tokens in
 // documents with prefixes, 16 heads: spans alone 181 us, with a bias 236; one kernel with run-time
-// switches took 285 there.  The instantiations are spread over several files, as each takes long to
+// switches took 285 there.  At 208 registers the softmax threads spill 12 words with the rule alone, 44
+// and 47 with a cap or a bias, 24 with both in bf16; 13, 53, 56 and 57 in e4m3 (-Xptxas -v).  The
+// instantiations are spread over several files, as each takes long to
 // compile.)
 template <bool kFp8, bool kMask, int kRules>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -9,10 +9,14 @@
 // The products run on mma.sync m16n8k16: 16 rows is the least a tensor instruction takes and
 // most batches fill only group x q_len of them, so the tensor pipe is far from the limit and a
 // 128-row tcgen05 tile would only add latency.
-//   bf16 cache  Q, P in bf16, ldmatrix from a 128-byte swizzled tile.
+//   bf16 cache  Q, P in bf16, ldmatrix from a 128-byte swizzled tile.  (P takes V's type, as both
+//               operands of a product have one: a rounding of 2^-8 a weight, that of the output.  The
+//               sum that divides O is of the weights before it, in 32 bits.)
 //   e4m3 cache  codes are widened to f16 in registers (exact); Q in f16 after a power-of-two scale
 //               per row that puts its largest value in [1, 2) (bf16 values stay exact down to
-//               2^-14 of it), P in f16, the head's scales in 32 bits outside the products.  K^T and V
+//               2^-14 of it), P in f16 (2^-11 a weight; those below 2^-25 of the piece's first
+//               maximum vanish from O, at most 2^-25 of the row's sum each), the head's scales
+//               in 32 bits outside the products.  K^T and V
 //               fragments are read by plain 16-byte shared loads: the order of the D dimension
 //               (for K) and of the keys in eights is permuted alike on both operands, so that each
 //               lane's bytes are contiguous and free of bank conflicts.  Bound by instruction issue

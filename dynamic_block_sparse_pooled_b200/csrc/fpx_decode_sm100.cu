@@ -6,7 +6,9 @@
 // the work is bound by the tensor cores, not by HBM (a 32768-token prompt behind 128 requests of 4
 // heads per KV head: 69 GFLOP, 134 MB; 88 us, 780 TFLOP/s, the tensor pipe 38 % busy: the softmax
 // chain of 2.5 us per pair of tiles sets the pace, and 10 us go into starting and the partials; an L2
-// prefetch four tiles ahead made it slower).  The pipeline is that of the prefill attention
+// prefetch four tiles ahead made it slower).  At 208 registers the softmax threads spill 96 words without
+// cap and bias, 59 to 79 with them (-Xptxas -v).  P is in bf16, as V is; its sum is of the weights
+// before that rounding.  The pipeline is that of the prefill attention
 // (fpx_attn_sm100.cuh): two 128-row tiles per CTA, S and O in TMEM, P over S, one warp that issues
 // every MMA in a fixed order, one that loads by TMA, two softmax warpgroups; K / V rings of two
 // 128-key slots.  A CTA's work is a stretch of the line of tiles (fpx_decode.cuh) instead of a unit.

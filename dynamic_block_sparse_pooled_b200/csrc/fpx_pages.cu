@@ -284,8 +284,9 @@ constexpr int kBatch = 4;  // rows of a thread in flight
 
 // A thread keeps one 16-byte chunk c of the row [hkv, d] (so its head's scale too) and walks over the
 // tokens, kBatch at a time; neighbouring threads have neighbouring chunks, so both sides are
-// contiguous per row.  blockIdx.y: K or V.  Bound by HBM (16384 rows of 8 x 128 from bf16 to e4m3: 101 MB
-// in 27 us, 3.7 TB/s; four rows in flight and no division of an index per chunk were worth 35 -> 27).
+// contiguous per row.  blockIdx.y: K or V.  16384 rows of 8 x 128 from bf16 to e4m3: 101 MB in 27 us, 3.7
+// TB/s; four rows in flight and no division of an index per chunk were worth 35 -> 27.  What bounds that
+// case is its waves: the e4m3 form takes 72 registers, so 444 of its 1184 CTAs are resident, 2.7 waves.
 template <bool kQuant>
 __global__ void __launch_bounds__(256) append_kernel(
     int tokens, int row_chunks, int chunks_per_head, const char* __restrict__ k, int64_t k_stride,

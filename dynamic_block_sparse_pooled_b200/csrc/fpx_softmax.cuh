@@ -141,8 +141,8 @@ __device__ __forceinline__ float capped_part_to_p(uint32_t* r, float k, const Ne
   return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-// Largest cap (log2 units) whose scores may all take tanh_ex2: 4e-7 of it is 2e-4, a tenth of a
-// bf16 weight's rounding.
+// Largest cap (log2 units) whose scores may all take tanh_ex2: 4e-7 of it is 2e-4, less than a
+// twentieth of a bf16 weight's rounding.
 constexpr float kEx2Cap = 512.f;
 
 // 64 columns of a row of S, the first of them column j0 of its key block, under a score rule: cap,
