@@ -48,9 +48,9 @@ ATTN_SOURCES = ("dynamic_block_sparse_pooled_b200/csrc/fpx_attn_sm100.cu",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_rule.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_sm100.cuh",
                 "dynamic_block_sparse_pooled_b200/csrc/fpx_common.cuh")
-ATTN_TRAFFIC_DIGEST = "a3978d45273cf2bed10370f18451224d9ea417207bc35772aac5243e97c895d5"
+ATTN_TRAFFIC_DIGEST = "8fda71147ce5f752b083ed2729757a7a997bad7885627e379b6b68e9494454f0"
 ATTN_TRAFFIC = {
-    "llama8b_bf16_n131072": 3299498240 + 1179589376,
+    "llama8b_bf16_n131072": 3304106240 + 1178298880,
 }
 
 
